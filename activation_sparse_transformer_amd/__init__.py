@@ -1,7 +1,8 @@
 """Activation-sparse ReLU FFN layer in TwELL form for AMD Instinct MI355X (gfx950).
 
 The compute lives in ``libsparse_ffn.so`` (hand-written HIP kernels behind a C ABI, see
-``include/sparse_ffn.h``); ``sparse_ffn`` is a thin ctypes binding to it.
+``include/sparse_ffn.h`` and ``include/ffn_ops.h``); ``sparse_ffn`` and ``ffn_ops`` are thin
+ctypes bindings to it: the layer, and the operators around it (norm, 4-bit products, AdamW).
 """
 from .sparse_ffn import (  # noqa: F401
     Config, SparseFFN, TwellBuffers, SffnError, twell_pack, twell_stats, check, buffer_sizes,
@@ -12,4 +13,7 @@ from .sparse_ffn import (  # noqa: F401
     SFFN_ERR_DEVICE, DOWN_AUTO, DOWN_GATHER, DOWN_MFMA, DOWN_TILES, DOWN_UNION, DOWN_SPARSE,
     DOWN_GATHER_DENSITY_DEFAULT, DOWN_MFMA_DENSITY_DEFAULT, DOWN_TILES_MIN_T, DOWN_MFMA_MIN_T,
     MAX_TILES,
+)
+from .ffn_ops import (  # noqa: F401
+    rms_norm, rms_norm_fp8, rms_norm_backward, mx4_quantize, Mx4Linear, AdamW,
 )

@@ -1,0 +1,208 @@
+// Gradient of the root-mean-square norm.  With xh = h rstd and t = dy gain:
+//
+//   dx = rstd (t - xh mean(t xh)) + dres,   dgain[c] = sum over rows of dy[., c] xh[., c]
+//
+// One pass over dy, h and dres: the L lanes of a row keep its elements in registers between the
+// row's sum and dx.  A lane sees the same columns in every row its group takes, so it sums
+// dgain in registers too; a workgroup joins its row groups in LDS in a fixed order and writes
+// one partial row, and a second kernel adds the partial rows in order (no atomics: the result
+// depends on the sizes alone).
+#include "ops_common.hpp"
+
+namespace sffn {
+namespace {
+
+template <typename T, typename G, int NV, int L>
+__global__ __launch_bounds__(L > 256 ? 1024 : 256) void rms_norm_grad_kernel(NormGradArgs a) {
+  constexpr int RPB = L < 256 ? 256 / L : 1;
+  __shared__ float red[2][L > 64 ? L / 64 : 1];
+  __shared__ float join[RPB > 1 ? RPB * 8 * L : 1];
+  const int li = (int)(threadIdx.x % L), grp = (int)(threadIdx.x / L);
+  const int d = a.d;
+  const bool tail = (d & 7) != 0;
+  const G* gain = static_cast<const G*>(a.gain);
+  const float inv_d = 1.f / (float)d;
+
+  Raw8<G> rg[NV];
+  float acc[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = (v * L + li) * 8;
+    rg[v].zero();
+    if (e + 8 <= d) rg[v].load(gain + e);
+    else if (e < d) rg[v].load_n(gain + e, d - e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[v][i] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows;
+       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+    const T* dres = static_cast<const T*>(a.dres) + row * a.dres_stride;
+    const float rstd = a.rstd[row];
+    Raw8<T> ry[NV], rh[NV], rr[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * L + li) * 8;
+      ry[v].zero();
+      rh[v].zero();
+      if (e + 8 <= d) {
+        ry[v].load(dy + e);
+        rh[v].load(h + e);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * L + li) * 8;
+      rr[v].zero();
+      if (a.dres && e + 8 <= d) rr[v].load(dres + e);
+    }
+    if (tail) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int e = (v * L + li) * 8;
+        if (e < d && e + 8 > d) {
+          ry[v].load_n(dy + e, d - e);
+          rh[v].load_n(h + e, d - e);
+          if (a.dres) rr[v].load_n(dres + e, d - e);
+        }
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = ry[v].get(i) * (rh[v].get(i) * rstd);
+        acc[v][i] += p;
+        dot += p * rg[v].get(i);
+      }
+    dot = row_reduce<L>(dot, Add(), red[turn]);
+    const float c = dot * inv_d;
+    T* dx = static_cast<T*>(a.dx) + row * d;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * L + li) * 8;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        o[i] = rstd * (ry[v].get(i) * rg[v].get(i) - rh[v].get(i) * rstd * c) + rr[v].get(i);
+      if (e + 8 <= d) store8(dx + e, o);
+      else if (e < d) store8_n(dx + e, o, d - e);
+    }
+  }
+  if (!a.dgain) return;
+  float* part = a.part + (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) join[grp * 8 * L + i * L + li] = acc[v][i];
+      __syncthreads();
+      for (int c = (int)threadIdx.x; c < 8 * L; c += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int g = 0; g < RPB; ++g) s += join[g * 8 * L + c];
+        const int col = (v * L + c % L) * 8 + c / L;
+        if (col < d) part[col] = s;
+      }
+    } else {
+      const int e = (v * L + li) * 8;
+      if (e + 8 <= d) store8(part + e, acc[v]);
+      else if (e < d) store8_n(part + e, acc[v], d - e);
+    }
+  }
+}
+
+// 32 columns of a workgroup; 32 row groups of 32 lanes each read every 32nd partial row.
+__global__ __launch_bounds__(1024) void rms_norm_grad_sum_kernel(const float* part, int n,
+                                                                 int32_t d, float* dgain) {
+  __shared__ float join[32][33];
+  const int c = (int)(threadIdx.x & 31), g = (int)(threadIdx.x >> 5);
+  const int col = (int)blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (col < d) {
+#pragma unroll 4
+    for (int r = g; r < n; r += 32) s += part[(int64_t)r * d + col];
+  }
+  join[g][c] = s;
+  __syncthreads();
+  if (g == 0 && col < d) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += join[i][c];
+    dgain[col] = t;
+  }
+}
+
+template <typename T, typename G, int L>
+hipError_t launch_nv(const NormGradArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)norm_grad_groups(a.rows, a.d)), block(L > 256 ? 1024 : 256);
+  const int nv = (a.d + 8 * L - 1) / (8 * L);
+#define SFFN_NV(n) \
+  case n: rms_norm_grad_kernel<T, G, n, L><<<grid, block, 0, s>>>(a); break
+  if constexpr (L < 64) {
+    switch (nv) {
+      SFFN_NV(1);
+      default: return hipErrorInvalidValue;
+    }
+  } else if constexpr (L == 1024) {
+    switch (nv) {
+      SFFN_NV(3);
+      SFFN_NV(4);
+      default: return hipErrorInvalidValue;
+    }
+  } else {
+    switch (nv) {
+      SFFN_NV(1);
+      SFFN_NV(2);
+      SFFN_NV(3);
+      SFFN_NV(4);
+      SFFN_NV(5);
+      SFFN_NV(6);
+      case 7:
+      SFFN_NV(8);
+      default: return hipErrorInvalidValue;
+    }
+  }
+#undef SFFN_NV
+  return hipGetLastError();
+}
+
+constexpr int WAVE_D = 2560;  // longest row that one wave takes
+
+template <typename T, typename G>
+hipError_t launch_t(const NormGradArgs& a, hipStream_t s) {
+  switch (norm_lanes(a.rows, a.d, WAVE_D)) {
+    case 16: return launch_nv<T, G, 16>(a, s);
+    case 32: return launch_nv<T, G, 32>(a, s);
+    case 64: return launch_nv<T, G, 64>(a, s);
+    case 256: return launch_nv<T, G, 256>(a, s);
+    default: return launch_nv<T, G, 1024>(a, s);
+  }
+}
+
+}  // namespace
+
+int norm_grad_groups(int64_t rows, int32_t d) {
+  const int L = norm_lanes(rows, d, WAVE_D);
+  const int rpb = L < 256 ? 256 / L : 1;
+  const int64_t need = (rows + rpb - 1) / rpb;
+  const int most = L > 256 ? 256 : 768;
+  return (int)(need < most ? need : most);
+}
+
+hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a, hipStream_t s) {
+  if (!bf16) return launch_t<float, float>(a, s);
+  return gain_f32 ? launch_t<uint16_t, float>(a, s) : launch_t<uint16_t, uint16_t>(a, s);
+}
+
+hipError_t launch_rms_norm_grad_sum(const float* part, int n, int32_t d, float* dgain,
+                                    hipStream_t s) {
+  rms_norm_grad_sum_kernel<<<dim3((unsigned)((d + 31) / 32)), 1024, 0, s>>>(part, n, d, dgain);
+  return hipGetLastError();
+}
+
+}  // namespace sffn

@@ -176,6 +176,24 @@ sffn_status_t check_bufs(const twell_buffers_t* b, bool need_all) {
 
 }  // namespace
 
+namespace sffn {
+sffn_status_t api_fail(sffn_status_t s, const char* msg) noexcept {
+  try {
+    return fail(s, msg);
+  } catch (...) {  // no memory for the message: the code alone is returned
+    return s;
+  }
+}
+sffn_status_t api_launch(const char* name, hipStream_t s, hipError_t (*f)(void*),
+                         void* ctx) noexcept {
+  try {
+    return run(name, s, [&] { return f(ctx); });
+  } catch (...) {
+    return SFFN_ERR_DEVICE;
+  }
+}
+}  // namespace sffn
+
 extern "C" {
 
 const char* sffn_status_string(sffn_status_t s) {

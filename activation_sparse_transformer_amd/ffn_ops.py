@@ -1,0 +1,412 @@
+"""Binding of the operators around the sparse FFN layer (the C ABI in include/ffn_ops.h): the
+RMS norm with the residual's sum and its gradient, products with 4-bit weights, AdamW.
+
+Argument marshalling only, as in ``sparse_ffn``: every step runs in the library's HIP kernels;
+PyTorch supplies device memory and the stream.  With ``stream=None`` a call runs on PyTorch's
+current stream of the tensors' device; a given ``stream`` is used for the kernels and for what
+the call allocates (inputs made on another stream have to be ready on it: the caller's events).
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import sparse_ffn as _base
+
+SFFN_E4M3 = 2
+NORM_MAX_D = 32768
+MX4_GROUP = 32
+ADAMW_BLOCK = 256
+
+_P = ctypes.c_void_p
+_I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_SZ = ctypes.c_size_t
+
+
+class AdamwTensorC(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")] + \
+               [("n", _I64)]
+
+
+class AdamwHyperC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+               [("step", _I64)]
+
+
+_NORM = [_I32, _I32, _P, _I64, _P, _I64, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _P]
+_PROTOS = {
+    "sffn_rms_norm": _NORM,
+    "sffn_rms_norm_fp8": _NORM,
+    "sffn_rms_norm_backward_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
+    "sffn_rms_norm_backward": [_I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I32, _P,
+                               _P, _P, _SZ, _P],
+    "sffn_mx4_quantize": [_I32, _P, _I64, _I32, _I32, _P, _P, _P],
+    "sffn_mx4_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
+    "sffn_mx4_tile": [_P, _P, _I32, _I32, _P, _P],
+    "sffn_mx4_linear": [_P, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _I32, _P, _P],
+    "sffn_adamw_step": [ctypes.POINTER(AdamwTensorC), _I32, _I32, _I32, _I32,
+                        ctypes.POINTER(AdamwHyperC), _P, _P],
+}
+
+_fns = None
+
+
+class _Fns:
+    pass
+
+
+def _lib():
+    """The entry points with their prototypes, looked up once."""
+    global _fns
+    if _fns is None:
+        import torch
+        L = _base.lib()
+        f = _Fns()
+        for name, args in _PROTOS.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
+            setattr(f, name, fn)
+        f.torch = torch
+        f.code = {torch.float32: _base.SFFN_F32, torch.bfloat16: _base.SFFN_BF16,
+                  torch.float8_e4m3fn: SFFN_E4M3}
+        _fns = f
+    return _fns
+
+
+def exported_names():
+    return list(_PROTOS)
+
+
+def _fail(status, where):
+    raise _base.SffnError(status, where, _base.last_error())
+
+
+class _On:
+    """Device and stream of a call: makes `device` current and, for a given stream, lets what
+    the call allocates belong to it."""
+
+    def __init__(self, torch, device, stream):
+        self.torch, self.stream, self.ctx = torch, stream, None
+        if device.type != "cuda":
+            raise ValueError("device tensors are needed")
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("stream is not of the tensors' device")
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        s = self.stream if self.stream is not None else self.torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _matrix(t, name, dtype, shape, device):
+    """Row stride of a [rows, d] tensor whose rows are contiguous."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on {device}")
+    s = t.stride()
+    if shape[1] > 1 and s[1] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if shape[0] > 1 and s[0] < shape[1]:
+        raise ValueError(f"the rows of {name} overlap")
+    return s[0] if shape[0] > 1 else shape[1]
+
+
+def _plain(t, name, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} "
+                         f"on {device}")
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm(fn, fp8, x, gain, residual, eps, y, stat, h, stream):
+    f = _lib()
+    torch = f.torch
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape = tuple(x.shape)
+    dev, dt = x.device, x.dtype
+    xs = _matrix(x, "x", dt, shape, dev)
+    rs = _matrix(residual, "residual", dt, shape, dev) if residual is not None else 0
+    if gain.dtype != dt and gain.dtype != torch.float32:
+        raise ValueError("gain must have x's type or float32")
+    _plain(gain, "gain", gain.dtype, (d,), dev)
+    if h is not None and residual is None:
+        raise ValueError("h is written only with a residual")
+    with _On(torch, dev, stream) as s:
+        out_t = torch.float8_e4m3fn if fp8 else dt
+        y = torch.empty(shape, dtype=out_t, device=dev) if y is None else \
+            _plain(y, "q" if fp8 else "y", out_t, shape, dev)
+        stat = torch.empty(rows, dtype=torch.float32, device=dev) if stat is None else \
+            _plain(stat, "scale" if fp8 else "rstd", torch.float32, (rows,), dev)
+        if residual is not None:
+            h = torch.empty(shape, dtype=dt, device=dev) if h is None else \
+                _plain(h, "h", dt, shape, dev)
+        st = getattr(f, fn)(f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs,
+                            gain.data_ptr(), eps, rows, d, y.data_ptr(), stat.data_ptr(), _ptr(h),
+                            s)
+    if st:
+        _fail(st, fn)
+    return y, stat, x if residual is None else h
+
+
+def rms_norm(x, gain, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream=None):
+    """h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * gain over the rows of
+    x [rows, d] (float32 or bfloat16; rows may be strided).  gain [d] has x's type or float32.
+    Returns (y, h, rstd): what rms_norm_backward takes; h is x without a residual.  y, h and
+    rstd may be given to be overwritten; h may be the (contiguous) residual or x itself."""
+    y, rstd, h = _norm("sffn_rms_norm", False, x, gain, residual, eps, y, rstd, h, stream)
+    return y, h, rstd
+
+
+def rms_norm_fp8(x, gain, residual=None, eps=1e-6, q=None, scale=None, h=None, stream=None):
+    """The norm for serving, its output in 8 bits: q [rows, d] float8_e4m3fn and scale [rows]
+    float32 (max |y| / 448 a row) with y ~ q * scale, as Mx4Linear takes them.  Returns
+    (q, scale, h)."""
+    return _norm("sffn_rms_norm_fp8", True, x, gain, residual, eps, q, scale, h, stream)
+
+
+def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dgain=None,
+                      stream=None):
+    """Gradient of rms_norm for dL/dy = dy, with the forward's h and rstd.  dres is the gradient
+    that reaches h past the norm (of the residual stream).  Returns (dx, dgain): dx, in h's
+    type, is the gradient of both x and the residual; dgain is float32, or None without
+    with_dgain.  dx may be given (also dres itself), and dgain."""
+    f = _lib()
+    torch = f.torch
+    if h.dim() != 2 or h.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("h must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape = tuple(h.shape)
+    dev, dt = h.device, h.dtype
+    hs = _matrix(h, "h", dt, shape, dev)
+    ys = _matrix(dy, "dy", dt, shape, dev)
+    rs = _matrix(dres, "dres", dt, shape, dev) if dres is not None else 0
+    if gain.dtype != dt and gain.dtype != torch.float32:
+        raise ValueError("gain must have h's type or float32")
+    _plain(gain, "gain", gain.dtype, (d,), dev)
+    _plain(rstd, "rstd", torch.float32, (rows,), dev)
+    with _On(torch, dev, stream) as s:
+        dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else \
+            _plain(dx, "dx", dt, shape, dev)
+        ws, nb = None, 0
+        if with_dgain:
+            dgain = torch.empty(d, dtype=torch.float32, device=dev) if dgain is None else \
+                _plain(dgain, "dgain", torch.float32, (d,), dev)
+            n = _SZ()
+            st = f.sffn_rms_norm_backward_workspace(rows, d, ctypes.byref(n))
+            if st:
+                _fail(st, "sffn_rms_norm_backward_workspace")
+            nb = n.value
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        else:
+            dgain = None
+        st = f.sffn_rms_norm_backward(f.code[dt], f.code[gain.dtype], dy.data_ptr(), ys,
+                                      h.data_ptr(), hs, gain.data_ptr(), rstd.data_ptr(),
+                                      _ptr(dres), rs, rows, d, dx.data_ptr(), _ptr(dgain),
+                                      _ptr(ws), nb, s)
+    if st:
+        _fail(st, "sffn_rms_norm_backward")
+    return dx, dgain
+
+
+def mx4_quantize(W, stream=None):
+    """(codes, scales) of a dense W [N, K] (float32 or bfloat16): uint8 [N, 16 * ceil(K / 32)]
+    with two e2m1 codes a byte (even k low) and uint8 [N, ceil(K / 32)] exponents + 127."""
+    f = _lib()
+    torch = f.torch
+    if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("W must be a float32 or bfloat16 tensor [N, K]")
+    N, K = W.shape
+    st_w = _matrix(W, "W", W.dtype, (N, K), W.device)
+    G = -(-K // MX4_GROUP)
+    with _On(torch, W.device, stream) as s:
+        codes = torch.empty((N, 16 * G), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((N, G), dtype=torch.uint8, device=W.device)
+        st = f.sffn_mx4_quantize(f.code[W.dtype], W.data_ptr(), st_w, N, K, codes.data_ptr(),
+                                 scales.data_ptr(), s)
+    if st:
+        _fail(st, "sffn_mx4_quantize")
+    return codes, scales
+
+
+class Mx4Linear:
+    """y = act(x W^T + bias) with 4-bit weights W [N, K], for batches of few tokens (serving).
+
+    codes and scales are as mx4_quantize gives them (MXFP4: e2m1 values, one power of two per 32
+    columns); in_features is K where it is not 32 * scales.shape[1].  They are laid out once for
+    the kernel, here, and not kept.  bias [N] float32 is borrowed (kept referenced)."""
+
+    def __init__(self, codes, scales, bias=None, relu=False, in_features=None, stream=None):
+        f = _lib()
+        torch = f.torch
+        if scales.dim() != 2 or scales.shape[1] < 1:
+            raise ValueError("scales must be [N, ceil(K / 32)]")
+        N, G = scales.shape
+        K = G * MX4_GROUP if in_features is None else int(in_features)
+        if not (G - 1) * MX4_GROUP < K <= G * MX4_GROUP:
+            raise ValueError(f"in_features must lie in ({(G - 1) * MX4_GROUP}, {G * MX4_GROUP}]")
+        dev = scales.device
+        _plain(scales, "scales", torch.uint8, (N, G), dev)
+        _plain(codes, "codes", torch.uint8, (N, 16 * G), dev)
+        if bias is not None:
+            _plain(bias, "bias", torch.float32, (N,), dev)
+        n = _SZ()
+        st = f.sffn_mx4_bytes(N, K, ctypes.byref(n))
+        if st:
+            _fail(st, "sffn_mx4_bytes")
+        with _On(torch, dev, stream) as s:
+            tiled = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            st = f.sffn_mx4_tile(codes.data_ptr(), scales.data_ptr(), N, K, tiled.data_ptr(), s)
+        if st:
+            _fail(st, "sffn_mx4_tile")
+        self.in_features, self.out_features = K, N
+        self.bias, self.relu, self.tiled, self.device = bias, bool(relu), tiled, dev
+
+    @classmethod
+    def from_dense(cls, W, bias=None, relu=False, stream=None):
+        """The layer of a dense W [N, K], quantised."""
+        codes, scales = mx4_quantize(W, stream=stream)
+        return cls(codes, scales, bias=bias, relu=relu, in_features=W.shape[1], stream=stream)
+
+    def __call__(self, x, x_scale=None, dtype=None, y=None, stream=None):
+        """x [T, K] is bfloat16, float32, or float8_e4m3fn with x_scale [T] float32 (which the
+        other types may have too).  y [T, N] is float32 or bfloat16: `dtype`, or that of a given
+        y; by default float32 for float32 x, otherwise bfloat16."""
+        f = _lib()
+        torch = f.torch
+        N, K, dev = self.out_features, self.in_features, self.device
+        xc = f.code.get(x.dtype)
+        if x.dim() != 2 or xc is None:
+            raise ValueError(f"x must be a float32, bfloat16 or float8_e4m3fn tensor [T, {K}]")
+        T = x.shape[0]
+        xs = _matrix(x, "x", x.dtype, (T, K), dev)
+        if x_scale is not None:
+            _plain(x_scale, "x_scale", torch.float32, (T,), dev)
+        elif xc == SFFN_E4M3:
+            raise ValueError("float8 x needs x_scale")
+        with _On(torch, dev, stream) as s:
+            if y is None:
+                dt = dtype or (torch.float32 if x.dtype == torch.float32 else torch.bfloat16)
+                if dt not in (torch.float32, torch.bfloat16):
+                    raise ValueError("dtype must be float32 or bfloat16")
+                y = torch.empty((T, N), dtype=dt, device=dev)
+            else:
+                if y.dtype not in (torch.float32, torch.bfloat16) or dtype not in (None, y.dtype):
+                    raise ValueError("y must be float32 or bfloat16, and of `dtype`")
+                _plain(y, "y", y.dtype, (T, N), dev)
+            st = f.sffn_mx4_linear(self.tiled.data_ptr(), N, K, xc, x.data_ptr(), xs,
+                                   _ptr(x_scale), T, _ptr(self.bias), self.relu, f.code[y.dtype],
+                                   y.data_ptr(), s)
+        if st:
+            _fail(st, "sffn_mx4_linear")
+        return y
+
+
+class AdamW:
+    """AdamW over a list of tensors, updated in place by one launch (per 48 tensors).
+
+    params: contiguous device tensors, all float32 or all bfloat16.  master: their float32
+    copies (for bfloat16 params), the values the step is taken on; params then receive the
+    rounded result.  state_bits 32 keeps both moments in float32; 8 keeps the first moment and
+    the root of the second as float8_e4m3fn with one float32 scale per 256 elements.  `state`
+    continues from given tensors instead of zeros: [m, v] or [m, m_scale, r, r_scale], each a
+    list like params; with it, state_bits goes by its length, and `step` is the number of steps
+    done.  The state tensors are in `.state`, in that order."""
+
+    def __init__(self, params, master=None, state_bits=32, state=None, lr=1e-3,
+                 betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=0):
+        f = _lib()
+        torch = f.torch
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        dt, dev = self.params[0].dtype, self.params[0].device
+        if dt not in (torch.float32, torch.bfloat16) or dev.type != "cuda":
+            raise ValueError("parameters must be float32 or bfloat16 device tensors")
+        for p in self.params:
+            _plain(p, "a parameter", dt, p.shape, dev)
+        self.master = None if master is None else list(master)
+        if self.master is not None and dt != torch.bfloat16:
+            raise ValueError("a master copy needs bfloat16 parameters")
+        if state is None:
+            if state_bits not in (8, 32):
+                raise ValueError("state_bits must be 8 or 32")
+            zeros = lambda t, n: [torch.zeros(n(p), dtype=t, device=dev) for p in self.params]  # noqa: E731
+            if state_bits == 32:
+                state = [zeros(torch.float32, lambda p: p.shape) for _ in range(2)]
+            else:
+                state = [zeros(t, n) for _ in range(2) for t, n in (
+                    (torch.float8_e4m3fn, lambda p: p.shape),
+                    (torch.float32, lambda p: -(-p.numel() // ADAMW_BLOCK)))]
+        self.state = [list(k) for k in state]
+        if len(self.state) not in (2, 4):
+            raise ValueError("state must be [m, v] or [m, m_scale, r, r_scale]")
+        self.state_bits = 32 if len(self.state) == 2 else 8
+        for k in self.state + ([] if self.master is None else [self.master]):
+            if len(k) != len(self.params):
+                raise ValueError("master and state must have one tensor for each parameter")
+        for i, p in enumerate(self.params):
+            if self.master is not None:
+                _plain(self.master[i], "a master copy", torch.float32, p.shape, dev)
+            for j, k in enumerate(self.state):
+                if self.state_bits == 32:
+                    _plain(k[i], "a state", torch.float32, p.shape, dev)
+                elif j % 2 == 0:
+                    _plain(k[i], "a state", torch.float8_e4m3fn, p.shape, dev)
+                else:
+                    _plain(k[i], "a state's scales", torch.float32,
+                           (-(-p.numel() // ADAMW_BLOCK),), dev)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.steps, self.device, self.dtype = int(step), dev, dt
+        self._t = (AdamwTensorC * len(self.params))()
+        for i, p in enumerate(self.params):
+            t = self._t[i]
+            t.param, t.n = p.data_ptr(), p.numel()
+            t.master = _ptr(self.master[i]) if self.master is not None else None
+            if self.state_bits == 32:
+                t.m, t.v = (k[i].data_ptr() for k in self.state)
+            else:
+                t.m, t.m_scale, t.v, t.v_scale = (k[i].data_ptr() for k in self.state)
+        self._code = f.code[dt]
+
+    def step(self, grads, grad_scale=None, stream=None):
+        """One step with grads (contiguous, shaped like params, all float32 or all bfloat16).
+        grad_scale, a float32 tensor of one element on the device, multiplies them (a clipping
+        or unscaling factor, without a wait for the host)."""
+        f = _lib()
+        torch = f.torch
+        if len(grads) != len(self.params):
+            raise ValueError("one gradient for each parameter is needed")
+        gt, dev = grads[0].dtype, self.device
+        if gt not in (torch.float32, torch.bfloat16):
+            raise ValueError("gradients must be float32 or bfloat16")
+        for t, p, g in zip(self._t, self.params, grads):
+            if g.dtype != gt or g.device != dev or g.shape != p.shape or not g.is_contiguous():
+                raise ValueError(f"a gradient must be a contiguous {gt} tensor of its "
+                                 f"parameter's shape on {dev}")
+            t.grad = g.data_ptr()
+        if grad_scale is not None and (grad_scale.dtype != torch.float32
+                                       or grad_scale.numel() != 1 or grad_scale.device != dev):
+            raise ValueError(f"grad_scale must be one float32 element on {dev}")
+        b1, b2 = self.betas
+        hp = AdamwHyperC(self.lr, b1, b2, self.eps, self.weight_decay, self.steps + 1)
+        with _On(torch, dev, stream) as s:
+            st = f.sffn_adamw_step(self._t, len(self.params), self._code, f.code[gt],
+                                   self.state_bits, ctypes.byref(hp), _ptr(grad_scale), s)
+        if st:
+            _fail(st, "sffn_adamw_step")
+        self.steps += 1

@@ -1,0 +1,164 @@
+"""Host-only checks of include/ffn_ops.h: every declared call is exported, wrapped and commented,
+constants agree with the binding, and bad arguments are refused before anything reaches the GPU.
+Runs without a GPU."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "ffn_ops.h")
+A = 0x1000  # stands for a device pointer; never followed
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+F32, BF16, E4M3 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def ops():
+    import activation_sparse_transformer_amd as sffn
+    from activation_sparse_transformer_amd import ffn_ops
+    if not os.path.exists(sffn.LIB_PATH):
+        pytest.fail("libsparse_ffn.so is not built (run __graft_entry__.build())")
+    return ffn_ops
+
+
+def test_header_matches_library_and_binding(ops):
+    text = open(HEADER).read()
+    code = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\bsffn_status_t\s+([a-z0-9_]+)\s*\(", code)))
+    assert names == sorted(ops.exported_names())
+    L = ctypes.CDLL(__import__("activation_sparse_transformer_amd").LIB_PATH)
+    for n in names:
+        assert hasattr(L, n), n
+        assert re.search(r"\*/\s*sffn_status_t\s+" + n + r"\s*\(", text), n
+    defs = dict(re.findall(r"#define\s+(SFFN_[A-Z0-9_]+)\s+([0-9]+)", code))
+    assert defs == {"SFFN_E4M3": str(ops.SFFN_E4M3), "SFFN_NORM_MAX_D": str(ops.NORM_MAX_D),
+                    "SFFN_MX4_GROUP": str(ops.MX4_GROUP), "SFFN_ADAMW_BLOCK": str(ops.ADAMW_BLOCK)}
+    assert ctypes.sizeof(ops.AdamwTensorC) == 64 and ctypes.sizeof(ops.AdamwHyperC) == 48
+
+
+NORM = dict(dtype=BF16, gain_dtype=BF16, x=A, x_stride=64, residual=A, residual_stride=64, gain=A,
+            eps=1e-6, rows=0, d=64, y=A, stat=A, h=A)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({}, OK), ({"dtype": 7}, INVALID), ({"dtype": E4M3}, INVALID), ({"gain_dtype": E4M3}, INVALID),
+    ({"dtype": F32, "gain_dtype": BF16}, INVALID), ({"gain_dtype": F32}, OK),
+    ({"d": 0}, INVALID), ({"d": -1}, INVALID), ({"d": 32769}, UNSUPPORTED), ({"rows": -1}, INVALID),
+    ({"eps": -1e-6}, INVALID), ({"eps": float("nan")}, INVALID), ({"residual": None}, INVALID),
+    ({"rows": 2, "x": None}, INVALID), ({"rows": 2, "x_stride": 63}, INVALID),
+    ({"rows": 2, "residual_stride": 0}, INVALID), ({"rows": 2, "gain": None}, INVALID),
+    ({"rows": 2, "y": None}, INVALID), ({"rows": 2, "x": A + 1}, INVALID),
+    ({"rows": 2, "h": A + 1}, INVALID), ({"rows": 2, "stat": A + 2}, INVALID),
+    ({"rows": 2, "gain": A + 1}, INVALID),
+])
+def test_norm_arguments(ops, kw, status):
+    a = dict(NORM, **kw)
+    for fn in ("sffn_rms_norm", "sffn_rms_norm_fp8"):
+        assert getattr(ops._lib(), fn)(*a.values(), None) == status, fn
+
+
+def test_norm_fp8_needs_scales(ops):
+    a = dict(NORM, rows=2, stat=None)
+    assert ops._lib().sffn_rms_norm_fp8(*a.values(), None) == INVALID
+
+
+GRAD = dict(dtype=BF16, gain_dtype=F32, dy=A, dy_stride=64, h=A, h_stride=64, gain=A, rstd=A, dres=A,
+            dres_stride=64, rows=2, d=64, dx=A, dgain=A, ws=A, nb=1 << 30)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"rows": 0, "dgain": None}, OK), ({"dtype": 5}, INVALID), ({"rows": -2}, INVALID),
+    ({"d": 40000}, UNSUPPORTED), ({"dy": None}, INVALID), ({"h": None}, INVALID),
+    ({"h_stride": 32}, INVALID), ({"dres_stride": 32}, INVALID), ({"rstd": None}, INVALID),
+    ({"dx": None}, INVALID), ({"ws": None}, INVALID), ({"ws": A + 8}, INVALID), ({"nb": 16}, INVALID),
+    ({"dx": A + 1}, INVALID), ({"dgain": A + 1}, INVALID),
+])
+def test_norm_backward_arguments(ops, kw, status):
+    a = dict(GRAD, **kw)
+    assert ops._lib().sffn_rms_norm_backward(*a.values(), None) == status
+
+
+def test_norm_workspace(ops):
+    f, n = ops._lib(), ctypes.c_size_t()
+    prev = 0
+    for rows in (0, 1, 4, 1000, 100000, 1 << 30):
+        assert f.sffn_rms_norm_backward_workspace(rows, 2048, ctypes.byref(n)) == OK
+        assert n.value % (2048 * 4) == 0 and n.value <= 1024 * 2048 * 4
+        assert (n.value == 0) == (rows == 0)
+        prev = max(prev, n.value)
+    assert f.sffn_rms_norm_backward_workspace(4, 2048, None) == INVALID
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"T": 0}, OK), ({"N": 0}, OK), ({"N": -1}, INVALID), ({"K": 0}, INVALID), ({"T": -1}, INVALID),
+    ({"T": (1 << 20) + 1}, UNSUPPORTED), ({"N": 1 << 30, "K": 1 << 20}, UNSUPPORTED),
+    ({"K": (1 << 30) + 1, "N": 1}, UNSUPPORTED), ({"x_dtype": 3}, INVALID), ({"y_dtype": E4M3}, INVALID),
+    ({"x_dtype": E4M3, "x_scale": None}, INVALID), ({"tiled": None}, INVALID), ({"tiled": A + 8}, INVALID),
+    ({"x": None}, INVALID), ({"x_stride": 63}, INVALID), ({"y": None}, INVALID), ({"y": A + 1}, INVALID),
+    ({"bias": A + 2}, INVALID), ({"x": A + 1}, INVALID),
+])
+def test_mx4_linear_arguments(ops, kw, status):
+    a = dict(tiled=A, N=48, K=64, x_dtype=BF16, x=A, x_stride=64, x_scale=A, T=3, bias=A, relu=1,
+             y_dtype=F32, y=A)
+    a.update(kw)
+    assert ops._lib().sffn_mx4_linear(*a.values(), None) == status
+
+
+def test_mx4_weights_arguments(ops):
+    f, n = ops._lib(), ctypes.c_size_t()
+    assert f.sffn_mx4_bytes(33, 129, ctypes.byref(n)) == OK and n.value == 3 * 2 * 1088
+    assert f.sffn_mx4_bytes(33, 129, None) == INVALID
+    assert f.sffn_mx4_tile(None, A, 16, 32, A, None) == INVALID
+    assert f.sffn_mx4_tile(A, A, 16, 32, A + 4, None) == INVALID
+    assert f.sffn_mx4_tile(A, A, 0, 32, None, None) == OK
+    assert f.sffn_mx4_quantize(E4M3, A, 32, 16, 32, A, A, None) == INVALID
+    assert f.sffn_mx4_quantize(F32, A, 31, 16, 32, A, A, None) == INVALID
+    assert f.sffn_mx4_quantize(F32, A, 32, 16, 32, A, None, None) == INVALID
+    assert f.sffn_mx4_quantize(F32, None, 32, 16, 32, A, A, None) == INVALID
+    assert f.sffn_mx4_quantize(F32, None, 32, 0, 32, None, None, None) == OK
+
+
+TENSOR = dict(param=A, grad=A, master=None, m=A, v=A, m_scale=A, v_scale=A, n=300)
+HYPER = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+
+
+@pytest.mark.parametrize("kw,hyper,types,status", [
+    ({"n": 0}, {}, (F32, F32, 32), OK), ({"n": 0, "param": None, "m": None}, {}, (F32, F32, 8), OK),
+    ({}, {}, (E4M3, F32, 32), INVALID), ({}, {}, (F32, E4M3, 32), INVALID), ({}, {}, (F32, F32, 16), INVALID),
+    ({"n": -1}, {}, (F32, F32, 32), INVALID), ({"param": None}, {}, (F32, F32, 32), INVALID),
+    ({"grad": None}, {}, (F32, F32, 32), INVALID), ({"m": None}, {}, (F32, F32, 32), INVALID),
+    ({"m_scale": None}, {}, (F32, F32, 8), INVALID), ({"master": A}, {}, (F32, F32, 32), INVALID),
+    ({"m": A + 2}, {}, (F32, F32, 32), INVALID), ({"param": A + 1}, {}, (BF16, F32, 32), INVALID),
+    ({}, {"beta1": 1.0}, (F32, F32, 32), INVALID), ({}, {"beta2": -0.1}, (F32, F32, 32), INVALID),
+    ({}, {"eps": -1.0}, (F32, F32, 32), INVALID), ({}, {"lr": float("inf")}, (F32, F32, 32), INVALID),
+    ({}, {"weight_decay": float("nan")}, (F32, F32, 32), INVALID), ({}, {"step": 0}, (F32, F32, 32), INVALID),
+])
+def test_adamw_arguments(ops, kw, hyper, types, status):
+    t = ops.AdamwTensorC(**dict(TENSOR, **kw))
+    h = ops.AdamwHyperC(**dict(HYPER, **hyper))
+    assert ops._lib().sffn_adamw_step(ctypes.byref(t), 1, *types, ctypes.byref(h), None, None) == status
+
+
+def test_adamw_lists(ops):
+    f = ops._lib()
+    h = ops.AdamwHyperC(**HYPER)
+    assert f.sffn_adamw_step(None, 0, F32, F32, 32, ctypes.byref(h), None, None) == OK
+    assert f.sffn_adamw_step(None, 1, F32, F32, 32, ctypes.byref(h), None, None) == INVALID
+    assert f.sffn_adamw_step(None, -1, F32, F32, 32, ctypes.byref(h), None, None) == INVALID
+    two = (ops.AdamwTensorC * 2)(ops.AdamwTensorC(**TENSOR), ops.AdamwTensorC(**dict(TENSOR, master=A)))
+    assert f.sffn_adamw_step(two, 2, BF16, F32, 32, ctypes.byref(h), None, None) == INVALID
+    assert f.sffn_adamw_step(two, 1, F32, F32, 32, None, None, None) == INVALID
+    assert f.sffn_adamw_step(two, 1, F32, F32, 32, ctypes.byref(h), A + 1, None) == INVALID
+
+
+def test_binding_needs_device_tensors(ops):
+    import torch
+    x, g = torch.zeros(2, 64), torch.ones(64)
+    for call in (lambda: ops.rms_norm(x, g), lambda: ops.rms_norm_fp8(x, g),
+                 lambda: ops.rms_norm_backward(x, x, g, torch.ones(2)), lambda: ops.mx4_quantize(x),
+                 lambda: ops.Mx4Linear(torch.zeros((2, 32), dtype=torch.uint8), torch.zeros((2, 2), dtype=torch.uint8)),
+                 lambda: ops.AdamW([x])):
+        with pytest.raises(ValueError):
+            call()
