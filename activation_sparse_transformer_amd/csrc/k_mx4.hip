@@ -28,83 +28,70 @@ __device__ __forceinline__ bf16x8 expand8(uint32_t codes, float scale) {
   return as_bf16x8(r);
 }
 
-// A lane's 32 consecutive columns of one token, and their bf16 products' operands.
+// Eight consecutive columns of one token, and their operands for the bf16 products.
 template <int XT>
-struct Tok;
+struct Tok8;
 template <>
-struct Tok<SFFN_BF16> {
+struct Tok8<SFFN_BF16> {
   static constexpr int TERMS = 1;
   typedef uint16_t elem;
-  u32x4 r[4];
-  __device__ __forceinline__ void zero() {
+  u32x4 r;
+  __device__ __forceinline__ void zero() { r = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const elem* p) { r = *reinterpret_cast<const u32x4_a2*>(p); }
+  __device__ __forceinline__ void load_n(const elem* p, int n) {  // n < 8, after zero()
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = u32x4{0, 0, 0, 0};
+    for (int j = 0; j < 8; ++j)
+      if (j < n) r[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
   }
-  __device__ __forceinline__ void load(const elem* p) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const u32x4_a2*>(p + 8 * j);
-  }
-  __device__ __forceinline__ void load_n(const elem* p, int n) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) r[j >> 3][(j & 7) >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-  }
-  __device__ __forceinline__ void terms(int j, bf16x8* t) const { t[0] = as_bf16x8(r[j]); }
+  __device__ __forceinline__ void terms(bf16x8* t) const { t[0] = as_bf16x8(r); }
 };
 template <>
-struct Tok<SFFN_E4M3> {
+struct Tok8<SFFN_E4M3> {
   static constexpr int TERMS = 1;
   typedef uint8_t elem;
-  u32x4 r[2];
-  __device__ __forceinline__ void zero() { r[0] = r[1] = u32x4{0, 0, 0, 0}; }
-  __device__ __forceinline__ void load(const elem* p) {
-    r[0] = *reinterpret_cast<const u32x4_a1*>(p);
-    r[1] = *reinterpret_cast<const u32x4_a1*>(p + 16);
-  }
+  u32x2 r;
+  __device__ __forceinline__ void zero() { r = u32x2{0, 0}; }
+  __device__ __forceinline__ void load(const elem* p) { r = *reinterpret_cast<const u32x2_a1*>(p); }
   __device__ __forceinline__ void load_n(const elem* p, int n) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) r[j >> 4][(j & 15) >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    for (int j = 0; j < 8; ++j)
+      if (j < n) r[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
   }
-  __device__ __forceinline__ void terms(int j, bf16x8* t) const {
+  __device__ __forceinline__ void terms(bf16x8* t) const {
     u32x4 o;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t w = r[j >> 1][(j & 1) * 2 + i];
-      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false));
-      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true));
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[i], 1.f, true));
     }
     t[0] = as_bf16x8(o);
   }
 };
 template <>
-struct Tok<SFFN_F32> {
+struct Tok8<SFFN_F32> {
   static constexpr int TERMS = 3;
   typedef float elem;
-  f32x4 r[8];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  f32x4 r[2];
+  __device__ __forceinline__ void zero() { r[0] = r[1] = f32x4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ void load(const elem* p) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = *reinterpret_cast<const f32x4_a4*>(p + 4 * j);
+    r[0] = *reinterpret_cast<const f32x4_a4*>(p);
+    r[1] = *reinterpret_cast<const f32x4_a4*>(p + 4);
   }
   __device__ __forceinline__ void load_n(const elem* p, int n) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < 8; ++j)
       if (j < n) r[j >> 2][j & 3] = p[j];
   }
   // x = hi + mid + lo, each the upper 16 bits of what is left; the rest of an infinity is 0
   // (its own difference would be NaN)
-  __device__ __forceinline__ void terms(int j, bf16x8* t) const {
+  __device__ __forceinline__ void terms(bf16x8* t) const {
     u32x4 o[3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t b[2][3];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float x = r[2 * j + (i >> 1)][(i & 1) * 2 + e];
+        const float x = r[i >> 1][(i & 1) * 2 + e];
         b[e][0] = __float_as_uint(x);
         const float hi = __uint_as_float(b[e][0] & 0xffff0000u);
         const float m = x == hi ? 0.f : x - hi;
@@ -120,17 +107,52 @@ struct Tok<SFFN_F32> {
   }
 };
 
+// Scale, bias and activation of four rows n .. n + 3 of one token, and their store.
+__device__ __forceinline__ void mx4_store(const Mx4Args& a, f32x4 s, int tok, int n) {
+  const int N = a.d.N;
+  if (tok >= a.T || n >= N) return;
+  const float xsc = a.x_scale ? a.x_scale[tok] : 1.f;
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float v = s[e] * xsc;
+    if (a.bias && n + e < N) v += a.bias[n + e];
+    o[e] = a.relu && v < 0.f ? 0.f : v;
+  }
+  const int64_t at = (int64_t)tok * N + n;
+  if (a.y_bf16) {
+    uint16_t* y = static_cast<uint16_t*>(a.y) + at;
+    if (n + 4 <= N) {
+      typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+      *reinterpret_cast<u32x2_a2*>(y) =
+          u32x2{(uint32_t)f32_to_bf16(o[0]) | ((uint32_t)f32_to_bf16(o[1]) << 16),
+                (uint32_t)f32_to_bf16(o[2]) | ((uint32_t)f32_to_bf16(o[3]) << 16)};
+    } else {
+      for (int e = 0; e < N - n; ++e) y[e] = f32_to_bf16(o[e]);
+    }
+  } else {
+    float* y = static_cast<float*>(a.y) + at;
+    if (n + 4 <= N) {
+      *reinterpret_cast<f32x4_a4*>(y) = f32x4{o[0], o[1], o[2], o[3]};
+    } else {
+      for (int e = 0; e < N - n; ++e) y[e] = o[e];
+    }
+  }
+}
+
 constexpr int MX4_WAVES = 8;
 
-// RB blocks of 16 weight rows and TT of 16 tokens a wave; U blocks of columns loaded together.
-template <int XT, int TT, int RB, int U>
+// RB blocks of 16 weight rows and TT of 16 tokens a wave; KS of a workgroup's waves split k, the
+// others take further rows.
+template <int XT, int TT, int RB, int KS>
 __global__ __launch_bounds__(MX4_WAVES * 64) void mx4_linear_kernel(Mx4Args a) {
-  typedef Tok<XT> X;
+  typedef Tok8<XT> X;
   typedef typename X::elem E;
   __shared__ f32x4 part[MX4_WAVES][RB][TT][64];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int q = lane >> 4, r = lane & 15;
-  const int rb0 = (int)blockIdx.x * RB, t0 = (int)blockIdx.y * (TT * 16);
+  const int wg0 = (int)blockIdx.x * (RB * MX4_WAVES / KS);
+  const int rb0 = wg0 + wave / KS * RB, t0 = (int)blockIdx.y * (TT * 16);
   const int KB = a.d.kb, K = a.d.K;
   const uint8_t* wb = static_cast<const uint8_t*>(a.tiled);
   const E* x = static_cast<const E*>(a.x);
@@ -141,63 +163,61 @@ __global__ __launch_bounds__(MX4_WAVES * 64) void mx4_linear_kernel(Mx4Args a) {
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int kb = wave; kb < KB; kb += MX4_WAVES * U) {
-    u32x4 c[U][RB];
-    uint32_t sc[U][RB];
-    X xs[U][TT];
+  for (int kb = wave % KS; kb < KB; kb += KS) {
+    u32x4 c[RB];
+    uint32_t sc[RB];
+    X xs[TT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = kb + u * MX4_WAVES;
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        c[u][b] = u32x4{0, 0, 0, 0};
-        sc[u][b] = 127;
-        if (k < KB && rb0 + b < a.d.nb) {
-          const uint8_t* p = wb + ((size_t)(rb0 + b) * KB + k) * MX4_BLOCK;
-          c[u][b] = *reinterpret_cast<const u32x4*>(p + lane * 16);
-          sc[u][b] = p[1024 + lane];
-        }
+    for (int b = 0; b < RB; ++b) {
+      c[b] = u32x4{0, 0, 0, 0};
+      sc[b] = 127;
+      if (rb0 + b < a.d.nb) {
+        const uint8_t* p = wb + ((size_t)(rb0 + b) * KB + kb) * MX4_BLOCK;
+        c[b] = *reinterpret_cast<const u32x4*>(p + lane * 16);
+        sc[b] = p[1024 + lane];
       }
     }
+    const int k0 = (kb * 4 + q) * 32;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k0 = ((kb + u * MX4_WAVES) * 4 + q) * 32;
+    for (int t = 0; t < TT; ++t) {
+      const int tok = t0 + t * 16 + r;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int tok = t0 + t * 16 + r;
-        xs[u][t].zero();
-        if (tok < a.T && k0 + 32 <= K) xs[u][t].load(x + (int64_t)tok * a.x_stride + k0);
+      for (int j = 0; j < 4; ++j) xs[t][j].zero();
+      if (tok < a.T && k0 + 32 <= K) {
+        const E* p = x + (int64_t)tok * a.x_stride + k0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xs[t][j].load(p + 8 * j);
       }
     }
     if (K & 31) {  // the last, partial group of 32 columns
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k0 = ((kb + u * MX4_WAVES) * 4 + q) * 32;
+      for (int t = 0; t < TT; ++t) {
+        const int tok = t0 + t * 16 + r;
+        if (tok < a.T && k0 < K && k0 + 32 > K) {
+          const E* p = x + (int64_t)tok * a.x_stride + k0;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int tok = t0 + t * 16 + r;
-          if (tok < a.T && k0 < K && k0 + 32 > K)
-            xs[u][t].load_n(x + (int64_t)tok * a.x_stride + k0, K - k0);
+          for (int j = 0; j < 4; ++j) {
+            const int n = K - k0 - 8 * j;
+            if (n >= 8) xs[t][j].load(p + 8 * j);
+            else if (n > 0) xs[t][j].load_n(p + 8 * j, n);
+          }
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int j = 0; j < 4; ++j) {
+      bf16x8 w[RB];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 w[RB];
+      for (int b = 0; b < RB; ++b) w[b] = expand8(c[b][j], __uint_as_float(sc[b] << 23));
 #pragma unroll
-        for (int b = 0; b < RB; ++b) w[b] = expand8(c[u][b][j], __uint_as_float(sc[u][b] << 23));
+      for (int t = 0; t < TT; ++t) {
+        bf16x8 xt[X::TERMS];
+        xs[t][j].terms(xt);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          bf16x8 xt[X::TERMS];
-          xs[u][t].terms(j, xt);
+        for (int k = X::TERMS - 1; k >= 0; --k)
 #pragma unroll
-          for (int k = X::TERMS - 1; k >= 0; --k)
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[b], xt[k], acc[b][t], 0, 0, 0);
-        }
+          for (int b = 0; b < RB; ++b)
+            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[b], xt[k], acc[b][t], 0, 0, 0);
       }
     }
   }
@@ -207,58 +227,61 @@ __global__ __launch_bounds__(MX4_WAVES * 64) void mx4_linear_kernel(Mx4Args a) {
     for (int t = 0; t < TT; ++t) part[wave][b][t][lane] = acc[b][t];
   __syncthreads();
 
-  const int N = a.d.N;
-  for (int i = (int)threadIdx.x; i < RB * TT * 64; i += MX4_WAVES * 64) {
-    const int l = i & 63, t = (i >> 6) % TT, b = (i >> 6) / TT;
-    f32x4 s = part[0][b][t][l];
+  constexpr int ITEMS = MX4_WAVES / KS * RB * TT * 64;
+  for (int i = (int)threadIdx.x; i < ITEMS; i += MX4_WAVES * 64) {
+    const int l = i & 63, t = (i >> 6) % TT, b = (i >> 6) / TT % RB, g = (i >> 6) / (TT * RB);
+    f32x4 s = part[g * KS][b][t][l];
 #pragma unroll
-    for (int w = 1; w < MX4_WAVES; ++w) s += part[w][b][t][l];
-    const int tok = t0 + t * 16 + (l & 15), n = (rb0 + b) * 16 + (l >> 4) * 4;
-    if (tok >= a.T || n >= N) continue;
-    const float xsc = a.x_scale ? a.x_scale[tok] : 1.f;
-    float o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = s[e] * xsc;
-      if (a.bias && n + e < N) v += a.bias[n + e];
-      o[e] = a.relu && v < 0.f ? 0.f : v;
-    }
-    const int64_t at = (int64_t)tok * N + n;
-    if (a.y_bf16) {
-      uint16_t* y = static_cast<uint16_t*>(a.y) + at;
-      if (n + 4 <= N) {
-        typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-        *reinterpret_cast<u32x2_a2*>(y) =
-            u32x2{(uint32_t)f32_to_bf16(o[0]) | ((uint32_t)f32_to_bf16(o[1]) << 16),
-                  (uint32_t)f32_to_bf16(o[2]) | ((uint32_t)f32_to_bf16(o[3]) << 16)};
-      } else {
-        for (int e = 0; e < N - n; ++e) y[e] = f32_to_bf16(o[e]);
-      }
-    } else {
-      float* y = static_cast<float*>(a.y) + at;
-      if (n + 4 <= N) {
-        *reinterpret_cast<f32x4_a4*>(y) = f32x4{o[0], o[1], o[2], o[3]};
-      } else {
-        for (int e = 0; e < N - n; ++e) y[e] = o[e];
-      }
-    }
+    for (int w = 1; w < KS; ++w) s += part[g * KS + w][b][t][l];
+    mx4_store(a, s, t0 + t * 16 + (l & 15), (wg0 + g * RB + b) * 16 + (l >> 4) * 4);
   }
 }
 
-template <int XT, int TT, int U>
-hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
-  constexpr int RB = 2;
-  const dim3 grid((unsigned)((a.d.nb + RB - 1) / RB), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
-  mx4_linear_kernel<XT, TT, RB, U><<<grid, MX4_WAVES * 64, 0, s>>>(a);
+template <int XT, int TT, int RB, int KS>
+hipError_t launch_ks(const Mx4Args& a, hipStream_t s) {
+  constexpr int ROWS = RB * MX4_WAVES / KS;
+  const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
+  mx4_linear_kernel<XT, TT, RB, KS><<<grid, MX4_WAVES * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int XT, int TT, int RB>
+hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
+  // Waves beyond the blocks of columns would idle: they take rows instead, while that leaves
+  // two workgroups a CU (65536 x 256, one token: 3.9 against 5.3 us).
+  int ks = MX4_WAVES;
+  while (ks > 2 && ks > a.d.kb && (int64_t)a.d.nb * ks / (2 * RB * MX4_WAVES) >= 256) ks /= 2;
+  if (ks == 8) return launch_ks<XT, TT, RB, 8>(a, s);
+  if (ks == 4) return launch_ks<XT, TT, RB, 4>(a, s);
+  return launch_ks<XT, TT, RB, 2>(a, s);
+}
+
+// A wave's work on a block of columns is that on its tokens (loads, conversions: about 1.5 TT
+// times what a block of weights costs, three times that for fp32) and on RB blocks of weights;
+// RB is the one with the least rounds of workgroups over the 256 CUs times that work.  Measured,
+// one token, K 2048, RB 1 / 2 / 4: N 2048 3.2 / 3.4 / 4.3 us, 8192 4.0 / 3.6 / 4.4; 12 tokens,
+// N 9216 - / 6.3 / 5.1, 65536 28.7 / 18.8 / 15.3.
+template <int XT, int TT>
+hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
+  const int64_t blocks = (int64_t)a.d.nb * ((a.T + TT * 16 - 1) / (TT * 16));
+  int best = 1;
+  double least = 0;
+  for (int rb = 1; rb <= 4; rb *= 2) {
+    const double cost = (double)((blocks + rb * 256 - 1) / (rb * 256)) *
+                        (1.5 * Tok8<XT>::TERMS * TT + rb);
+    if (rb == 1 || cost < least) {
+      best = rb;
+      least = cost;
+    }
+  }
+  if (best == 1) return launch_rb<XT, TT, 1>(a, s);
+  if (best == 2) return launch_rb<XT, TT, 2>(a, s);
+  return launch_rb<XT, TT, 4>(a, s);
 }
 
 template <int XT>
 hipError_t launch_x(const Mx4Args& a, hipStream_t s) {
-  constexpr bool F = XT == SFFN_F32;
-  if (a.T <= 16) return launch_tt<XT, 1, F ? 2 : 4>(a, s);
-  if (a.T <= 32) return launch_tt<XT, 2, F ? 1 : 2>(a, s);
-  return launch_tt<XT, 4, 1>(a, s);
+  return a.T <= 16 ? launch_tt<XT, 1>(a, s) : launch_tt<XT, 2>(a, s);
 }
 
 // ------------------------------------------------------------------ weights
