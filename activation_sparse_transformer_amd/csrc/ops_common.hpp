@@ -1,6 +1,8 @@
 // Device helpers and launchers of the operators around the layer (include/ffn_ops.h).
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/ffn_ops.h"
 #include "sffn_common.hpp"
 
@@ -152,14 +154,11 @@ __device__ __forceinline__ float inv_rms(float ms) { return 1.f / sqrtf(ms); }
 #endif
 
 // ---------------------------------------------------------------- launchers
-// Lanes that share a row of d elements in the norm kernels, 8 elements each: 16 and 32 for
-// short rows, a wave while there are enough rows (`many`) to fill the GPU with a wave each,
-// four waves for fewer or longer rows, sixteen beyond what four hold in registers.
-inline int norm_lanes(int64_t rows, int32_t d, int32_t wave_d) {
-  if (d <= 128) return 16;
-  if (d <= 256) return 32;
-  if (d <= 512 || (d <= wave_d && rows >= 1024)) return 64;
-  return d <= 16384 ? 256 : 1024;
+// Lanes that share a row of d elements in the norm kernels; a lane keeps 8, 16, or (16 waves)
+// up to 32 of them.  Few elements a lane leave registers for many rows in flight: 8192 x 4096
+// takes 46 us with 4 waves a row and 51 with one (gradient 54 and 69), 16384 x 1024 27 and 25.
+inline int norm_lanes(int32_t d) {
+  return d <= 128 ? 16 : d <= 256 ? 32 : d <= 1024 ? 64 : d <= 4096 ? 256 : 1024;
 }
 struct NormArgs {
   const void* x;
@@ -174,6 +173,25 @@ struct NormArgs {
   float* stat;  // rstd, or the 8-bit scales
   void* h;
 };
+// Calls f(lanes, vectors of 8 a lane) with both as integral constants, for a row of d elements.
+template <typename F>
+hipError_t norm_shape(int32_t d, F&& f) {
+  const int L = norm_lanes(d), nv = (d + 8 * L - 1) / (8 * L);
+#define SFFN_SHAPE(l, n) \
+  if (L == l && nv == n) return f(std::integral_constant<int, l>(), std::integral_constant<int, n>())
+  SFFN_SHAPE(16, 1);
+  SFFN_SHAPE(32, 1);
+  SFFN_SHAPE(64, 1);
+  SFFN_SHAPE(64, 2);
+  SFFN_SHAPE(256, 1);
+  SFFN_SHAPE(256, 2);
+  SFFN_SHAPE(1024, 1);
+  SFFN_SHAPE(1024, 2);
+  SFFN_SHAPE(1024, 3);
+  SFFN_SHAPE(1024, 4);
+#undef SFFN_SHAPE
+  return hipErrorInvalidValue;
+}
 hipError_t launch_rms_norm(bool bf16, bool gain_f32, bool fp8, const NormArgs& a, hipStream_t s);
 
 struct NormGradArgs {
