@@ -8,7 +8,12 @@ the call allocates (inputs made on another stream have to be ready on it: the ca
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+from operator import attrgetter
+
+import numpy as np
 
 from . import sparse_ffn as _base
 
@@ -32,6 +37,9 @@ class AdamwHyperC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
                [("step", _I64)]
 
+
+_GRAD_WORD = AdamwTensorC.grad.offset // 8
+_SHAPE, _DTYPE = attrgetter("shape"), attrgetter("dtype")
 
 _NORM = [_I32, _I32, _P, _I64, _P, _I64, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _P]
 _PROTOS = {
@@ -68,6 +76,11 @@ def _lib():
             fn.restype = ctypes.c_int
             setattr(f, name, fn)
         f.torch = torch
+        f.current_device = torch.cuda.current_device
+        # the current stream's handle of a device index (without making a Stream object, where
+        # this torch has the call)
+        f.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
         f.code = {torch.float32: _base.SFFN_F32, torch.bfloat16: _base.SFFN_BF16,
                   torch.float8_e4m3fn: SFFN_E4M3}
         _fns = f
@@ -82,36 +95,32 @@ def _fail(status, where):
     raise _base.SffnError(status, where, _base.last_error())
 
 
-class _On:
-    """Device and stream of a call: makes `device` current and, for a given stream, lets what
-    the call allocates belong to it."""
+def _elsewhere(f, device, stream):
+    """Whether a call has to enter `_on` first: a stream is given, or `device` is not current."""
+    if device.index is None:
+        raise ValueError("device tensors are needed")
+    return stream is not None or device.index != f.current_device()
 
-    def __init__(self, torch, device, stream):
-        self.torch, self.stream, self.ctx = torch, stream, None
-        if device.type != "cuda":
-            raise ValueError("device tensors are needed")
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("stream is not of the tensors' device")
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        s = self.stream if self.stream is not None else self.torch.cuda.current_stream()
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+@contextlib.contextmanager
+def _on(device, stream):
+    """Makes `device`, and `stream` if given, current: what the call allocates belongs to it."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("device tensors are needed")
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+    else:
+        if stream.device != device:
+            raise ValueError("stream is not of the tensors' device")
+        with torch.cuda.stream(stream):
+            yield
 
 
 def _matrix(t, name, dtype, shape, device):
     """Row stride of a [rows, d] tensor whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.device != device or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on {device}")
     s = t.stride()
     if shape[1] > 1 and s[1] != 1:
@@ -122,8 +131,7 @@ def _matrix(t, name, dtype, shape, device):
 
 
 def _plain(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) \
-            or not t.is_contiguous():
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} "
                          f"on {device}")
     return t
@@ -136,31 +144,39 @@ def _ptr(t):
 def _norm(fn, fp8, x, gain, residual, eps, y, stat, h, stream):
     f = _lib()
     torch = f.torch
-    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
-    rows, d = shape = tuple(x.shape)
     dev, dt = x.device, x.dtype
+    if _elsewhere(f, dev, stream):
+        with _on(dev, stream):
+            return _norm(fn, fp8, x, gain, residual, eps, y, stat, h, None)
+    shape = x.shape
+    if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape
     xs = _matrix(x, "x", dt, shape, dev)
     rs = _matrix(residual, "residual", dt, shape, dev) if residual is not None else 0
     if gain.dtype != dt and gain.dtype != torch.float32:
         raise ValueError("gain must have x's type or float32")
     _plain(gain, "gain", gain.dtype, (d,), dev)
-    if h is not None and residual is None:
-        raise ValueError("h is written only with a residual")
-    with _On(torch, dev, stream) as s:
-        out_t = torch.float8_e4m3fn if fp8 else dt
-        y = torch.empty(shape, dtype=out_t, device=dev) if y is None else \
-            _plain(y, "q" if fp8 else "y", out_t, shape, dev)
-        stat = torch.empty(rows, dtype=torch.float32, device=dev) if stat is None else \
-            _plain(stat, "scale" if fp8 else "rstd", torch.float32, (rows,), dev)
-        if residual is not None:
-            h = torch.empty(shape, dtype=dt, device=dev) if h is None else \
-                _plain(h, "h", dt, shape, dev)
-        st = getattr(f, fn)(f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs,
-                            gain.data_ptr(), eps, rows, d, y.data_ptr(), stat.data_ptr(), _ptr(h),
-                            s)
+    out_t = torch.float8_e4m3fn if fp8 else dt
+    if y is not None:
+        _plain(y, "q" if fp8 else "y", out_t, shape, dev)
+    else:
+        y = x.new_empty(shape, dtype=out_t) if fp8 or xs != d else torch.empty_like(x)
+    stat = x.new_empty(rows, dtype=torch.float32) if stat is None else \
+        _plain(stat, "scale" if fp8 else "rstd", torch.float32, (rows,), dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only with a residual")
+    else:
+        if h is not None:
+            _plain(h, "h", dt, shape, dev)
+        else:
+            h = torch.empty_like(residual) if rs == d else residual.new_empty(shape)
+    st = fn(f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs,
+            gain.data_ptr(), eps, rows, d, y.data_ptr(), stat.data_ptr(), _ptr(h),
+            f.stream(dev.index))
     if st:
-        _fail(st, fn)
+        _fail(st, "sffn_rms_norm_fp8" if fp8 else "sffn_rms_norm")
     return y, stat, x if residual is None else h
 
 
@@ -169,7 +185,7 @@ def rms_norm(x, gain, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream
     x [rows, d] (float32 or bfloat16; rows may be strided).  gain [d] has x's type or float32.
     Returns (y, h, rstd): what rms_norm_backward takes; h is x without a residual.  y, h and
     rstd may be given to be overwritten; h may be the (contiguous) residual or x itself."""
-    y, rstd, h = _norm("sffn_rms_norm", False, x, gain, residual, eps, y, rstd, h, stream)
+    y, rstd, h = _norm(_lib().sffn_rms_norm, False, x, gain, residual, eps, y, rstd, h, stream)
     return y, h, rstd
 
 
@@ -177,7 +193,7 @@ def rms_norm_fp8(x, gain, residual=None, eps=1e-6, q=None, scale=None, h=None, s
     """The norm for serving, its output in 8 bits: q [rows, d] float8_e4m3fn and scale [rows]
     float32 (max |y| / 448 a row) with y ~ q * scale, as Mx4Linear takes them.  Returns
     (q, scale, h)."""
-    return _norm("sffn_rms_norm_fp8", True, x, gain, residual, eps, q, scale, h, stream)
+    return _norm(_lib().sffn_rms_norm_fp8, True, x, gain, residual, eps, q, scale, h, stream)
 
 
 def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dgain=None,
@@ -188,10 +204,14 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
     with_dgain.  dx may be given (also dres itself), and dgain."""
     f = _lib()
     torch = f.torch
-    if h.dim() != 2 or h.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("h must be a float32 or bfloat16 tensor [rows, d]")
-    rows, d = shape = tuple(h.shape)
     dev, dt = h.device, h.dtype
+    if _elsewhere(f, dev, stream):
+        with _on(dev, stream):
+            return rms_norm_backward(dy, h, gain, rstd, dres, with_dgain, dx, dgain)
+    shape = h.shape
+    if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("h must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape
     hs = _matrix(h, "h", dt, shape, dev)
     ys = _matrix(dy, "dy", dt, shape, dev)
     rs = _matrix(dres, "dres", dt, shape, dev) if dres is not None else 0
@@ -199,28 +219,34 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
         raise ValueError("gain must have h's type or float32")
     _plain(gain, "gain", gain.dtype, (d,), dev)
     _plain(rstd, "rstd", torch.float32, (rows,), dev)
-    with _On(torch, dev, stream) as s:
-        dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else \
-            _plain(dx, "dx", dt, shape, dev)
-        ws, nb = None, 0
-        if with_dgain:
-            dgain = torch.empty(d, dtype=torch.float32, device=dev) if dgain is None else \
-                _plain(dgain, "dgain", torch.float32, (d,), dev)
-            n = _SZ()
-            st = f.sffn_rms_norm_backward_workspace(rows, d, ctypes.byref(n))
-            if st:
-                _fail(st, "sffn_rms_norm_backward_workspace")
-            nb = n.value
-            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        else:
-            dgain = None
-        st = f.sffn_rms_norm_backward(f.code[dt], f.code[gain.dtype], dy.data_ptr(), ys,
-                                      h.data_ptr(), hs, gain.data_ptr(), rstd.data_ptr(),
-                                      _ptr(dres), rs, rows, d, dx.data_ptr(), _ptr(dgain),
-                                      _ptr(ws), nb, s)
+    if dx is not None:
+        _plain(dx, "dx", dt, shape, dev)
+    else:
+        dx = torch.empty_like(h) if hs == d else h.new_empty(shape)
+    ws, nb = None, 0
+    if with_dgain:
+        dgain = torch.empty(d, dtype=torch.float32, device=dev) if dgain is None else \
+            _plain(dgain, "dgain", torch.float32, (d,), dev)
+        nb = _norm_workspace(rows, d)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    else:
+        dgain = None
+    st = f.sffn_rms_norm_backward(f.code[dt], f.code[gain.dtype], dy.data_ptr(), ys,
+                                  h.data_ptr(), hs, gain.data_ptr(), rstd.data_ptr(),
+                                  _ptr(dres), rs, rows, d, dx.data_ptr(), _ptr(dgain),
+                                  _ptr(ws), nb, f.stream(dev.index))
     if st:
         _fail(st, "sffn_rms_norm_backward")
     return dx, dgain
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(rows, d):
+    n = _SZ()
+    st = _lib().sffn_rms_norm_backward_workspace(rows, d, ctypes.byref(n))
+    if st:
+        _fail(st, "sffn_rms_norm_backward_workspace")
+    return n.value
 
 
 def mx4_quantize(W, stream=None):
@@ -228,16 +254,18 @@ def mx4_quantize(W, stream=None):
     with two e2m1 codes a byte (even k low) and uint8 [N, ceil(K / 32)] exponents + 127."""
     f = _lib()
     torch = f.torch
+    if _elsewhere(f, W.device, stream):
+        with _on(W.device, stream):
+            return mx4_quantize(W)
     if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("W must be a float32 or bfloat16 tensor [N, K]")
     N, K = W.shape
     st_w = _matrix(W, "W", W.dtype, (N, K), W.device)
     G = -(-K // MX4_GROUP)
-    with _On(torch, W.device, stream) as s:
-        codes = torch.empty((N, 16 * G), dtype=torch.uint8, device=W.device)
-        scales = torch.empty((N, G), dtype=torch.uint8, device=W.device)
-        st = f.sffn_mx4_quantize(f.code[W.dtype], W.data_ptr(), st_w, N, K, codes.data_ptr(),
-                                 scales.data_ptr(), s)
+    codes = torch.empty((N, 16 * G), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((N, G), dtype=torch.uint8, device=W.device)
+    st = f.sffn_mx4_quantize(f.code[W.dtype], W.data_ptr(), st_w, N, K, codes.data_ptr(),
+                             scales.data_ptr(), f.stream(W.device.index))
     if st:
         _fail(st, "sffn_mx4_quantize")
     return codes, scales
@@ -268,13 +296,15 @@ class Mx4Linear:
         st = f.sffn_mx4_bytes(N, K, ctypes.byref(n))
         if st:
             _fail(st, "sffn_mx4_bytes")
-        with _On(torch, dev, stream) as s:
+        with _on(dev, stream):
             tiled = torch.empty(n.value, dtype=torch.uint8, device=dev)
-            st = f.sffn_mx4_tile(codes.data_ptr(), scales.data_ptr(), N, K, tiled.data_ptr(), s)
+            st = f.sffn_mx4_tile(codes.data_ptr(), scales.data_ptr(), N, K, tiled.data_ptr(),
+                                 f.stream(dev.index))
         if st:
             _fail(st, "sffn_mx4_tile")
         self.in_features, self.out_features = K, N
         self.bias, self.relu, self.tiled, self.device = bias, bool(relu), tiled, dev
+        self._tiled_ptr, self._bias_ptr = tiled.data_ptr(), _ptr(bias)
 
     @classmethod
     def from_dense(cls, W, bias=None, relu=False, stream=None):
@@ -289,28 +319,32 @@ class Mx4Linear:
         f = _lib()
         torch = f.torch
         N, K, dev = self.out_features, self.in_features, self.device
+        if _elsewhere(f, dev, stream):
+            with _on(dev, stream):
+                return self(x, x_scale, dtype, y)
+        shape = x.shape
         xc = f.code.get(x.dtype)
-        if x.dim() != 2 or xc is None:
+        if len(shape) != 2 or xc is None:
             raise ValueError(f"x must be a float32, bfloat16 or float8_e4m3fn tensor [T, {K}]")
-        T = x.shape[0]
+        T = shape[0]
         xs = _matrix(x, "x", x.dtype, (T, K), dev)
         if x_scale is not None:
             _plain(x_scale, "x_scale", torch.float32, (T,), dev)
         elif xc == SFFN_E4M3:
             raise ValueError("float8 x needs x_scale")
-        with _On(torch, dev, stream) as s:
-            if y is None:
-                dt = dtype or (torch.float32 if x.dtype == torch.float32 else torch.bfloat16)
-                if dt not in (torch.float32, torch.bfloat16):
-                    raise ValueError("dtype must be float32 or bfloat16")
-                y = torch.empty((T, N), dtype=dt, device=dev)
-            else:
-                if y.dtype not in (torch.float32, torch.bfloat16) or dtype not in (None, y.dtype):
-                    raise ValueError("y must be float32 or bfloat16, and of `dtype`")
-                _plain(y, "y", y.dtype, (T, N), dev)
-            st = f.sffn_mx4_linear(self.tiled.data_ptr(), N, K, xc, x.data_ptr(), xs,
-                                   _ptr(x_scale), T, _ptr(self.bias), self.relu, f.code[y.dtype],
-                                   y.data_ptr(), s)
+        if y is None:
+            dt = dtype or (torch.float32 if xc == _base.SFFN_F32 else torch.bfloat16)
+            if dt not in (torch.float32, torch.bfloat16):
+                raise ValueError("dtype must be float32 or bfloat16")
+            y = torch.empty((T, N), dtype=dt, device=dev)
+        else:
+            dt = y.dtype
+            if dt not in (torch.float32, torch.bfloat16) or dtype not in (None, dt):
+                raise ValueError("y must be float32 or bfloat16, and of `dtype`")
+            _plain(y, "y", dt, (T, N), dev)
+        st = f.sffn_mx4_linear(self._tiled_ptr, N, K, xc, x.data_ptr(), xs, _ptr(x_scale), T,
+                               self._bias_ptr, self.relu, f.code[dt], y.data_ptr(),
+                               f.stream(dev.index))
         if st:
             _fail(st, "sffn_mx4_linear")
         return y
@@ -382,6 +416,9 @@ class AdamW:
             else:
                 t.m, t.m_scale, t.v, t.v_scale = (k[i].data_ptr() for k in self.state)
         self._code = f.code[dt]
+        self._shapes = [p.shape for p in self.params]
+        # the same table as words, for the column of gradient pointers
+        self._words = np.frombuffer(self._t, dtype=np.uint64).reshape(len(self.params), -1)
 
     def step(self, grads, grad_scale=None, stream=None):
         """One step with grads (contiguous, shaped like params, all float32 or all bfloat16).
@@ -389,24 +426,30 @@ class AdamW:
         or unscaling factor, without a wait for the host)."""
         f = _lib()
         torch = f.torch
+        dev = self.device
+        if _elsewhere(f, dev, stream):
+            with _on(dev, stream):
+                return self.step(grads, grad_scale)
         if len(grads) != len(self.params):
             raise ValueError("one gradient for each parameter is needed")
-        gt, dev = grads[0].dtype, self.device
+        gt = grads[0].dtype
         if gt not in (torch.float32, torch.bfloat16):
             raise ValueError("gradients must be float32 or bfloat16")
-        for t, p, g in zip(self._t, self.params, grads):
-            if g.dtype != gt or g.device != dev or g.shape != p.shape or not g.is_contiguous():
-                raise ValueError(f"a gradient must be a contiguous {gt} tensor of its "
-                                 f"parameter's shape on {dev}")
-            t.grad = g.data_ptr()
+        T = torch.Tensor
+        if list(map(_SHAPE, grads)) != self._shapes or set(map(_DTYPE, grads)) != {gt} \
+                or set(map(T.get_device, grads)) != {dev.index} \
+                or not all(map(T.is_contiguous, grads)):
+            raise ValueError(f"gradients must be contiguous {gt} tensors of their parameters' "
+                             f"shapes on {dev}")
         if grad_scale is not None and (grad_scale.dtype != torch.float32
                                        or grad_scale.numel() != 1 or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one float32 element on {dev}")
+        self._words[:, _GRAD_WORD] = list(map(T.data_ptr, grads))
         b1, b2 = self.betas
         hp = AdamwHyperC(self.lr, b1, b2, self.eps, self.weight_decay, self.steps + 1)
-        with _On(torch, dev, stream) as s:
-            st = f.sffn_adamw_step(self._t, len(self.params), self._code, f.code[gt],
-                                   self.state_bits, ctypes.byref(hp), _ptr(grad_scale), s)
+        st = f.sffn_adamw_step(self._t, len(self.params), self._code, f.code[gt],
+                               self.state_bits, ctypes.byref(hp), _ptr(grad_scale),
+                               f.stream(dev.index))
         if st:
             _fail(st, "sffn_adamw_step")
         self.steps += 1
