@@ -4,16 +4,19 @@
 // One wave holds 16 x 128 weights in a 16-byte load a lane (the tiled layout: 1 KB contiguous),
 // expands them to bf16 with the packed conversion that applies the scale (exact: a bf16 holds
 // e2m1 times a power of two) and multiplies on the matrix cores: A = 16 weight rows, B = up to
-// 16 tokens, v_mfma_f32_16x16x32_bf16.  Which k a lane's eight elements stand for is the same
-// permutation for both operands, so a lane's 32 consecutive columns make four such products.
-// Token types: bf16 as it is; e4m3 widened to bf16 (exact); fp32 as the sum of three bf16
-// (truncations: 8 + 8 + 8 bits, exact), three products.  The waves of a workgroup split k and
-// add their fp32 sums in LDS in wave order.
+// 16 tokens, v_mfma_f32_16x16x32_bf16, four for a block.  Token types: bf16 as it is; e4m3
+// widened to bf16 (exact); fp32 as the sum of three bf16 (truncations: 8 + 8 + 8 bits, exact),
+// three products.  (The scaled 8-bit x 4-bit matrix instruction would need no expansion, but its
+// sums over 128 columns came out up to 1e-4 of the absolute products off; these are fp32.)
+// The waves of a workgroup split k and add their fp32 sums in LDS in wave order.
+//
+// Bound by reading the weights at few tokens: 65536 x 8192 at 4 tokens 49.8 us (5.7 TB/s).
 #include "ops_common.hpp"
 
 namespace sffn {
 namespace {
 
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
@@ -107,6 +110,50 @@ struct Tok8<SFFN_F32> {
   }
 };
 
+// 16 tokens x 128 columns on their way to the matrix cores.  A product wants lane (q, r) to hold
+// token r, so its own loads would touch 16 rows in every group of 16 lanes, which costs four
+// times a contiguous load: a wave loads whole rows instead (LPR lanes a row) and turns them in
+// its own piece of LDS.  16-byte units are permuted within a row (by the token) so that neither
+// side conflicts.
+template <int XT>
+struct TokTile {
+  typedef typename Tok8<XT>::elem E;
+  static constexpr int LPR = 8 * (int)sizeof(E);  // lanes of a row
+  static constexpr int RPL = 64 / LPR;            // rows of a load
+  static constexpr int LOADS = 16 / RPL;
+  static constexpr int BYTES = 16 * 128 * (int)sizeof(E);
+  u32x4 v[LOADS];
+
+  // tokens t0 .. t0 + 15 (those past the last one are not needed: the last one, or nothing)
+  __device__ __forceinline__ void load(const E* x, int64_t stride, int t0, int T, int k0, int lane) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      if (t0 + i * RPL >= T) break;
+      const int t = t0 + i * RPL + lane / LPR;
+      const E* p = x + (int64_t)(t < T ? t : T - 1) * stride + k0 + lane % LPR * (128 / LPR);
+      v[i] = *reinterpret_cast<const u32x4_a1*>(p);
+    }
+  }
+  static __device__ __forceinline__ int unit(int t, int u) { return t * LPR + (u ^ (t & (LPR < 16 ? LPR - 1 : 15))); }
+  __device__ __forceinline__ void put(u32x4* lds, int lane) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) lds[unit(i * RPL + lane / LPR, lane % LPR)] = v[i];
+  }
+  // columns 32 j + 8 q .. + 7 of token r
+  static __device__ __forceinline__ Tok8<XT> get(const u32x4* lds, int j, int q, int r) {
+    Tok8<XT> o;
+    if constexpr (XT == SFFN_BF16) {
+      o.r = lds[unit(r, 4 * j + q)];
+    } else if constexpr (XT == SFFN_F32) {
+      o.r[0] = __builtin_bit_cast(f32x4, lds[unit(r, 8 * j + 2 * q)]);
+      o.r[1] = __builtin_bit_cast(f32x4, lds[unit(r, 8 * j + 2 * q + 1)]);
+    } else {
+      o.r = reinterpret_cast<const u32x2*>(lds + unit(r, 2 * j + (q >> 1)))[q & 1];
+    }
+    return o;
+  }
+};
+
 // Scale, bias and activation of four rows n .. n + 3 of one token, and their store.
 __device__ __forceinline__ void mx4_store(const Mx4Args& a, f32x4 s, int tok, int n) {
   const int N = a.d.N;
@@ -142,97 +189,143 @@ __device__ __forceinline__ void mx4_store(const Mx4Args& a, f32x4 s, int tok, in
 
 constexpr int MX4_WAVES = 8;
 
-// RB blocks of 16 weight rows and TT of 16 tokens a wave; KS of a workgroup's waves split k, the
-// others take further rows.
-template <int XT, int TT, int RB, int KS>
-__global__ __launch_bounds__(MX4_WAVES * 64) void mx4_linear_kernel(Mx4Args a) {
-  typedef Tok8<XT> X;
-  typedef typename X::elem E;
-  __shared__ f32x4 part[MX4_WAVES][RB][TT][64];
-  const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
-  const int q = lane >> 4, r = lane & 15;
-  const int wg0 = (int)blockIdx.x * (RB * MX4_WAVES / KS);
-  const int rb0 = wg0 + wave / KS * RB, t0 = (int)blockIdx.y * (TT * 16);
-  const int KB = a.d.kb, K = a.d.K;
-  const uint8_t* wb = static_cast<const uint8_t*>(a.tiled);
-  const E* x = static_cast<const E*>(a.x);
+// Orders a wave's accesses to its own piece of LDS: the hardware carries them out in order, only
+// the compiler has to keep it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
-  f32x4 acc[RB][TT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+// A wave's weights of one block of 128 columns: RB blocks of 16 rows.
+template <int RB>
+struct Mx4Weights {
+  u32x4 c[RB];
+  uint32_t sc[RB];
 
-  for (int kb = wave % KS; kb < KB; kb += KS) {
-    u32x4 c[RB];
-    uint32_t sc[RB];
-    X xs[TT][4];
+  __device__ __forceinline__ void load(const uint8_t* const* w, int kb, int lane) {
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      c[b] = u32x4{0, 0, 0, 0};
-      sc[b] = 127;
-      if (rb0 + b < a.d.nb) {
-        const uint8_t* p = wb + ((size_t)(rb0 + b) * KB + kb) * MX4_BLOCK;
-        c[b] = *reinterpret_cast<const u32x4*>(p + lane * 16);
-        sc[b] = p[1024 + lane];
-      }
+      const uint8_t* p = w[b] + (size_t)kb * MX4_BLOCK;
+      c[b] = *reinterpret_cast<const u32x4*>(p + lane * 16);
+      sc[b] = *reinterpret_cast<const uint32_t*>(p + 1024 + (lane & 15) * 4);
     }
-    const int k0 = (kb * 4 + q) * 32;
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int tok = t0 + t * 16 + r;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xs[t][j].zero();
-      if (tok < a.T && k0 + 32 <= K) {
-        const E* p = x + (int64_t)tok * a.x_stride + k0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xs[t][j].load(p + 8 * j);
-      }
-    }
-    if (K & 31) {  // the last, partial group of 32 columns
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int tok = t0 + t * 16 + r;
-        if (tok < a.T && k0 < K && k0 + 32 > K) {
-          const E* p = x + (int64_t)tok * a.x_stride + k0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = K - k0 - 8 * j;
-            if (n >= 8) xs[t][j].load(p + 8 * j);
-            else if (n > 0) xs[t][j].load_n(p + 8 * j, n);
-          }
-        }
-      }
-    }
+  }
+  // token(j, t): the lane's columns of word j of token tile t
+  template <int XT, int TT, typename F>
+  __device__ __forceinline__ void product(f32x4 (&acc)[RB][TT], F token) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf16x8 w[RB];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) w[b] = expand8(c[b][j], __uint_as_float(sc[b] << 23));
+      for (int b = 0; b < RB; ++b)
+        w[b] = expand8(c[b][j], __uint_as_float(((sc[b] >> (8 * j)) & 0xffu) << 23));
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        bf16x8 xt[X::TERMS];
-        xs[t][j].terms(xt);
+        bf16x8 xt[Tok8<XT>::TERMS];
+        token(j, t).terms(xt);
 #pragma unroll
-        for (int k = X::TERMS - 1; k >= 0; --k)
+        for (int k = Tok8<XT>::TERMS - 1; k >= 0; --k)
 #pragma unroll
           for (int b = 0; b < RB; ++b)
             acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[b], xt[k], acc[b][t], 0, 0, 0);
       }
     }
   }
+};
+
+// KS of a workgroup's waves split k, the others take further rows.  Rows past the end are read as
+// the last one and not stored; what a column without a token holds is not stored either (a
+// product's columns do not mix).  More than 16 tokens are turned in LDS; up to 16 each lane loads
+// its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048).
+// Many waves hide the loads: a second block of columns in flight in a wave gained nothing.
+template <int XT, int TT, int RB, int KS>
+__global__ __launch_bounds__(MX4_WAVES * 64, RB * TT <= 4 ? 4 : 2) void mx4_linear_kernel(Mx4Args a) {
+  typedef TokTile<XT> Tile;
+  typedef typename Tile::E E;
+  constexpr bool TURN = TT > 1;
+  constexpr int UNITS = TURN ? TT * Tile::BYTES / 16 : 0;  // of a wave's tokens
+  constexpr int PART = RB * TT * 64;            // of a wave's sums
+  __shared__ u32x4 lds[MX4_WAVES * (UNITS > PART ? UNITS : PART)];
+  const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
+  const int q = lane >> 4, r = lane & 15;
+  const int wg0 = (int)blockIdx.x * (RB * MX4_WAVES / KS);
+  const int rb0 = wg0 + wave / KS * RB, t0 = (int)blockIdx.y * (TT * 16);
+  const int K = a.d.K, whole = K / 128;
+  const E* x = static_cast<const E*>(a.x);
+
+  const uint8_t* w[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int rb = rb0 + b < a.d.nb ? rb0 + b : a.d.nb - 1;
+    w[b] = static_cast<const uint8_t*>(a.tiled) + (size_t)rb * a.d.kb * MX4_BLOCK;
+  }
+  f32x4 acc[RB][TT];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) part[wave][b][t][lane] = acc[b][t];
-  __syncthreads();
+    for (int t = 0; t < TT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  constexpr int ITEMS = MX4_WAVES / KS * RB * TT * 64;
-  for (int i = (int)threadIdx.x; i < ITEMS; i += MX4_WAVES * 64) {
-    const int l = i & 63, t = (i >> 6) % TT, b = (i >> 6) / TT % RB, g = (i >> 6) / (TT * RB);
-    f32x4 s = part[g * KS][b][t][l];
+  if constexpr (TURN) {
+    u32x4* own = lds + wave * UNITS;
+    for (int kb = wave % KS; kb < whole; kb += KS) {
+      Mx4Weights<RB> wt;
+      Tile tile[TT];
 #pragma unroll
-    for (int w = 1; w < KS; ++w) s += part[g * KS + w][b][t][l];
+      for (int t = 0; t < TT; ++t) tile[t].load(x, a.x_stride, t0 + t * 16, a.T, kb * 128, lane);
+      wt.load(w, kb, lane);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) tile[t].put(own + t * (Tile::BYTES / 16), lane);
+      wave_fence();
+      wt.template product<XT, TT>(acc, [&](int j, int t) {
+        return Tile::get(own + t * (Tile::BYTES / 16), j, q, r);
+      });
+      wave_fence();
+    }
+  } else {
+    const E* x_row = x + (int64_t)(t0 + r) * a.x_stride + q * 8;
+    const bool have = t0 + r < a.T;
+    Tok8<XT> tok[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tok[j].zero();
+    for (int kb = wave % KS; kb < whole; kb += KS) {
+      Mx4Weights<RB> wt;
+      wt.load(w, kb, lane);
+      if (have) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tok[j].load(x_row + kb * 128 + 32 * j);
+      }
+      wt.template product<XT, TT>(acc, [&](int j, int) { return tok[j]; });
+    }
+  }
+  if (whole < a.d.kb && wave % KS == whole % KS) {  // the last, partial block of columns
+    Mx4Weights<RB> wt;
+    wt.load(w, whole, lane);
+    wt.template product<XT, TT>(acc, [&](int j, int t) {
+      const int tok = t0 + t * 16 + r, k0 = whole * 128 + 32 * j + 8 * q, n = K - k0;
+      Tok8<XT> o;
+      o.zero();
+      if (tok < a.T && n > 0) {
+        const E* p = x + (int64_t)tok * a.x_stride + k0;
+        if (n >= 8) o.load(p);
+        else o.load_n(p, n);
+      }
+      return o;
+    });
+  }
+
+  __syncthreads();  // the sums take the tokens' place
+  f32x4* part = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[wave * PART + (b * TT + t) * 64 + lane] = acc[b][t];
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < MX4_WAVES / KS * PART; i += MX4_WAVES * 64) {
+    const int g = i / PART, at = i % PART, l = at & 63, t = (at >> 6) % TT, b = (at >> 6) / TT;
+    f32x4 s = part[g * KS * PART + at];
+#pragma unroll
+    for (int v = 1; v < KS; ++v) s += part[(g * KS + v) * PART + at];
     mx4_store(a, s, t0 + t * 16 + (l & 15), (wg0 + g * RB + b) * 16 + (l >> 4) * 4);
   }
 }
@@ -247,20 +340,22 @@ hipError_t launch_ks(const Mx4Args& a, hipStream_t s) {
 
 template <int XT, int TT, int RB>
 hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
-  // Waves beyond the blocks of columns would idle: they take rows instead, while that leaves
-  // two workgroups a CU (65536 x 256, one token: 3.9 against 5.3 us).
+  // Waves that split k cost a join, and idle beyond the blocks of columns; they take rows
+  // instead while that leaves enough workgroups (65536 x 256, one token: 3.9 against 5.3 us;
+  // 65536 x 2048, 64 tokens in 8 bits: 28 against 33).
+  constexpr int64_t ENOUGH = TT > 1 ? 256 : 512;
   int ks = MX4_WAVES;
-  while (ks > 2 && ks > a.d.kb && (int64_t)a.d.nb * ks / (2 * RB * MX4_WAVES) >= 256) ks /= 2;
+  while (ks > 2 && (int64_t)a.d.nb * ks / (2 * RB * MX4_WAVES) >= ENOUGH) ks /= 2;
   if (ks == 8) return launch_ks<XT, TT, RB, 8>(a, s);
   if (ks == 4) return launch_ks<XT, TT, RB, 4>(a, s);
   return launch_ks<XT, TT, RB, 2>(a, s);
 }
 
-// A wave's work on a block of columns is that on its tokens (loads, conversions: about 1.5 TT
-// times what a block of weights costs, three times that for fp32) and on RB blocks of weights;
-// RB is the one with the least rounds of workgroups over the 256 CUs times that work.  Measured,
-// one token, K 2048, RB 1 / 2 / 4: N 2048 3.2 / 3.4 / 4.3 us, 8192 4.0 / 3.6 / 4.4; 12 tokens,
-// N 9216 - / 6.3 / 5.1, 65536 28.7 / 18.8 / 15.3.
+// A wave's work on a block of columns is that on its tokens (loads, conversions: one and a half
+// times a block of weights', four times for fp32) and on RB blocks of weights; RB is the one
+// with the least rounds of workgroups over the 256 CUs times that work.  Measured, one token,
+// K 2048, RB 1 / 2 / 4: N 2048 3.0 / 3.4 / 4.2 us, 8192 4.0 / 3.6 / 4.3; 64 tokens in 8 bits, N
+// 8192 7.8 / 6.6 / 8.8, 9216 (K 2304) 11.8 / 12.2 / 9.6, 65536 45 / 35 / 28.
 template <int XT, int TT>
 hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
   const int64_t blocks = (int64_t)a.d.nb * ((a.T + TT * 16 - 1) / (TT * 16));
@@ -268,7 +363,7 @@ hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
   double least = 0;
   for (int rb = 1; rb <= 4; rb *= 2) {
     const double cost = (double)((blocks + rb * 256 - 1) / (rb * 256)) *
-                        (1.5 * Tok8<XT>::TERMS * TT + rb);
+                        ((XT == SFFN_F32 ? 4.0 : 1.5) + rb);
     if (rb == 1 || cost < least) {
       best = rb;
       least = cost;
@@ -281,7 +376,10 @@ hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
 
 template <int XT>
 hipError_t launch_x(const Mx4Args& a, hipStream_t s) {
-  return a.T <= 16 ? launch_tt<XT, 1>(a, s) : launch_tt<XT, 2>(a, s);
+  if (a.T <= 16) return launch_tt<XT, 1>(a, s);
+  // fp32 tokens for 64 would not fit the LDS
+  if (XT == SFFN_F32 || a.T <= 32) return launch_tt<XT, 2>(a, s);
+  return launch_tt<XT, XT == SFFN_F32 ? 2 : 4>(a, s);
 }
 
 // ------------------------------------------------------------------ weights
@@ -338,27 +436,23 @@ __global__ __launch_bounds__(256) void mx4_tile_kernel(const uint8_t* codes, con
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t blk = i >> 6;
   if (blk >= (int64_t)d.nb * d.kb) return;
-  const int lane = (int)(i & 63);
-  const int64_t n = blk / d.kb * 16 + (lane & 15);
-  const int g = (int)(blk % d.kb) * 4 + (lane >> 4), G = (d.K + 31) / 32;
+  const int lane = (int)(i & 63), q = lane >> 4, G = (d.K + 31) / 32;
+  const int64_t row0 = blk / d.kb * 16, n = row0 + (lane & 15);
+  const int g0 = (int)(blk % d.kb) * 4;
   u32x4 c = u32x4{0, 0, 0, 0};
-  uint8_t sc = 127;
-  if (n < d.N && g < G) {
-    c = *reinterpret_cast<const u32x4_a1*>(codes + (n * G + g) * 16);
-    sc = scales[n * G + g];
-    const int len = d.K - g * 32;
-    if (len < 32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int left = len - 8 * j;
-        if (left <= 0) c[j] = 0;
-        else if (left < 8) c[j] &= (1u << (4 * left)) - 1;
-      }
-    }
+  for (int j = 0; j < 4; ++j) {
+    if (n >= d.N || g0 + j >= G) continue;
+    c[j] = *reinterpret_cast<const u32_a1*>(codes + (n * G + g0 + j) * 16 + q * 4);
+    const int len = d.K - (g0 + j) * 32 - q * 8;  // codes past the columns' end: 0
+    if (len <= 0) c[j] = 0;
+    else if (len < 8) c[j] &= (1u << (4 * len)) - 1;
   }
   uint8_t* p = tiled + blk * MX4_BLOCK;
   *reinterpret_cast<u32x4*>(p + lane * 16) = c;
-  p[1024 + lane] = sc;
+  const int64_t sn = row0 + (lane >> 2);  // scales: row by row, the block's four groups each
+  const int sg = g0 + (lane & 3);
+  p[1024 + lane] = sn < d.N && sg < G ? scales[sn * G + sg] : 127;
 }
 
 }  // namespace

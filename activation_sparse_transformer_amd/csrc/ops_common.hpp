@@ -216,8 +216,9 @@ hipError_t launch_rms_norm_grad_sum(const float* part, int n, int32_t d, float* 
                                     hipStream_t s);
 
 // The tiled 4-bit layout: for every 16 rows and 128 columns a block of MX4_BLOCK bytes: 1 KB of
-// codes (lane l of a wave: row l % 16, the 32 columns of group l / 16), then their 64 scales in
-// the same order.  Blocks run over the columns first.
+// codes (lane l of a wave: row l % 16, word j of its four: columns 32 j + 8 (l / 16) and the
+// seven after), then 64 scales (row by row, the four groups of 32 columns).  Blocks run over the
+// columns first.
 constexpr int MX4_BLOCK = 1024 + 64;
 struct Mx4Dims {
   int32_t N, K;
