@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "entry.hpp"
 #include "ops_common.hpp"
 
 using namespace sffn;

@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "entry.hpp"
 #include "sffn_common.hpp"
 
 using namespace sffn;

@@ -203,16 +203,6 @@ __device__ __forceinline__ void note_choice(const DownHint& h, int n_blocks, boo
 }
 #endif
 
-// ---------------------------------------------------------------- entry-point helpers
-// Shared by the files that implement C entry points: record the calling thread's error
-// message and return `s`; launch f under the kernel name `name` (timed while profiling is on).
-sffn_status_t api_fail(sffn_status_t s, const char* msg) noexcept;
-sffn_status_t api_launch(const char* name, hipStream_t s, hipError_t (*f)(void*), void* ctx) noexcept;
-template <typename Fn>
-inline sffn_status_t api_run(const char* name, hipStream_t s, Fn& f) noexcept {
-  return api_launch(name, s, [](void* c) -> hipError_t { return (*static_cast<Fn*>(c))(); }, &f);
-}
-
 // ---------------------------------------------------------------- launchers
 // Each returns the launch's hipError_t (hipGetLastError after the launch).
 hipError_t launch_pack(const Dims& d, const float* h, const twell_buffers_t& b,
