@@ -234,13 +234,20 @@ struct Mx4Weights {
   }
 };
 
+// Whether two workgroups fit a CU: 128 registers and half of the LDS do without spilling.
+template <int XT, int TT, int RB>
+constexpr bool mx4_pairs() {
+  return TT == 1 || (XT == SFFN_E4M3 && RB * TT <= (TT == 2 ? 6 : 8)) ||
+         (XT == SFFN_BF16 && RB * TT <= 4 && TT == 2);
+}
+
 // KS of a workgroup's waves split k, the others take further rows.  Rows past the end are read as
 // the last one and not stored; what a column without a token holds is not stored either (a
 // product's columns do not mix).  More than 16 tokens are turned in LDS; up to 16 each lane loads
 // its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048).
 // Many waves hide the loads: a second block of columns in flight in a wave gained nothing.
 template <int XT, int TT, int RB, int KS>
-__global__ __launch_bounds__(MX4_WAVES * 64, RB * TT <= 4 ? 4 : 2) void mx4_linear_kernel(Mx4Args a) {
+__global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs<XT, TT, RB>() ? 4 : 2)) void mx4_linear_kernel(Mx4Args a) {
   typedef TokTile<XT> Tile;
   typedef typename Tile::E E;
   constexpr bool TURN = TT > 1;
@@ -338,48 +345,73 @@ hipError_t launch_ks(const Mx4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+int64_t mx4_token_groups(const Mx4Args& a, int TT) { return (a.T + TT * 16 - 1) / (TT * 16); }
+
 template <int XT, int TT, int RB>
 hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
   // Waves that split k cost a join, and idle beyond the blocks of columns; they take rows
   // instead while that leaves enough workgroups (65536 x 256, one token: 3.9 against 5.3 us;
   // 65536 x 2048, 64 tokens in 8 bits: 28 against 33).
   constexpr int64_t ENOUGH = TT > 1 ? 256 : 512;
+  const int64_t blocks = a.d.nb * mx4_token_groups(a, TT);
   int ks = MX4_WAVES;
-  while (ks > 2 && (int64_t)a.d.nb * ks / (2 * RB * MX4_WAVES) >= ENOUGH) ks /= 2;
+  while (ks > 2 && blocks * ks / (2 * RB * MX4_WAVES) >= ENOUGH) ks /= 2;
   if (ks == 8) return launch_ks<XT, TT, RB, 8>(a, s);
   if (ks == 4) return launch_ks<XT, TT, RB, 4>(a, s);
   return launch_ks<XT, TT, RB, 2>(a, s);
 }
 
-// A wave's work on a block of columns is that on its tokens (loads, conversions: one and a half
-// times a block of weights', four times for fp32) and on RB blocks of weights; RB is the one
-// with the least rounds of workgroups over the 256 CUs times that work.  Measured, one token,
-// K 2048, RB 1 / 2 / 4: N 2048 3.0 / 3.4 / 4.2 us, 8192 4.0 / 3.6 / 4.3; 64 tokens in 8 bits, N
-// 8192 7.8 / 6.6 / 8.8, 9216 (K 2304) 11.8 / 12.2 / 9.6, 65536 45 / 35 / 28.
+// Estimated time of a tile shape, in units of a wave's work on one block of 16 rows, 128 columns
+// and up to 32 tokens: per block of columns that on the tokens (loads, conversions) and on RB
+// blocks of weights, for as many workgroups as a CU gets, and for every workgroup (for every
+// two where two fit at once) the 10 units, 2 us, that its loads and its join take to pass.  Four
+// tiles of tokens cost 1.7 times two (the weights are expanded once) and 16 units.  Fitted to sweeps of RB and
+// TT over N 2048 .. 65536, K 256 .. 8192.
+template <int XT, int TT, int RB>
+double mx4_cost(const Mx4Args& a) {
+  const double tokens = XT == SFFN_F32 ? 4.0 : TT == 1 ? 2.2 : XT == SFFN_BF16 ? 3.0 : 1.5;
+  const int64_t groups = (a.d.nb * mx4_token_groups(a, TT) + RB - 1) / RB, n = (groups + 255) / 256;
+  const int64_t turns = mx4_pairs<XT, TT, RB>() ? (n + 1) / 2 : n;
+  const double blocks = a.d.kb > MX4_WAVES ? (double)a.d.kb / MX4_WAVES : 1.0;
+  return (TT == 4 ? 16.0 : 10.0) * (double)turns + (double)n * blocks * (tokens + RB) * (TT == 4 ? 1.7 : 1.0);
+}
 template <int XT, int TT>
-hipError_t launch_tt(const Mx4Args& a, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.d.nb * ((a.T + TT * 16 - 1) / (TT * 16));
-  int best = 1;
-  double least = 0;
-  for (int rb = 1; rb <= 4; rb *= 2) {
-    const double cost = (double)((blocks + rb * 256 - 1) / (rb * 256)) *
-                        ((XT == SFFN_F32 ? 4.0 : 1.5) + rb);
-    if (rb == 1 || cost < least) {
-      best = rb;
-      least = cost;
-    }
+double mx4_best(const Mx4Args& a, int* rb) {
+  const double c[4] = {mx4_cost<XT, TT, 1>(a), mx4_cost<XT, TT, 2>(a), mx4_cost<XT, TT, 3>(a),
+                       mx4_cost<XT, TT, 4>(a)};
+  *rb = 1;
+  for (int i = 2; i <= 4; ++i)
+    if (c[i - 1] < c[*rb - 1]) *rb = i;
+  return c[*rb - 1];
+}
+
+// The row blocks with the least estimated time.  Measured, RB 1 / 2 / 4: one token, K 2048: N 2048
+// 3.0 / 3.4 / 4.2 us, 8192 4.0 / 3.6 / 4.3; 64 tokens in 8 bits (TT 2), RB 1 / 2 / 3 / 4: N 8192 8.0 /
+// 6.3 / 7.9 / 6.1, 9216 (K 2304) 10.6 / 10.3 / 8.0 / 10.7.
+template <int XT, int TT>
+hipError_t launch_tt(const Mx4Args& a, int rb, hipStream_t s) {
+  switch (rb) {
+    case 1: return launch_rb<XT, TT, 1>(a, s);
+    case 2: return launch_rb<XT, TT, 2>(a, s);
+    case 3: return launch_rb<XT, TT, 3>(a, s);
+    default: return launch_rb<XT, TT, 4>(a, s);
   }
-  if (best == 1) return launch_rb<XT, TT, 1>(a, s);
-  if (best == 2) return launch_rb<XT, TT, 2>(a, s);
-  return launch_rb<XT, TT, 4>(a, s);
 }
 
 template <int XT>
 hipError_t launch_x(const Mx4Args& a, hipStream_t s) {
-  if (a.T <= 16) return launch_tt<XT, 1>(a, s);
-  // fp32 tokens for 64 would not fit the LDS
-  if (XT == SFFN_F32 || a.T <= 32) return launch_tt<XT, 2>(a, s);
-  return launch_tt<XT, XT == SFFN_F32 ? 2 : 4>(a, s);
+  int rb = 1, rb4 = 1;
+  if (a.T <= 16) {
+    mx4_best<XT, 1>(a, &rb);
+    return launch_tt<XT, 1>(a, rb, s);
+  }
+  const double two = mx4_best<XT, 2>(a, &rb);
+  if constexpr (XT != SFFN_F32) {  // (four tiles of fp32 tokens would not fit the LDS)
+    // 64 tokens at once read and expand the weights once: 32768 x 2048 in 8 bits 16 us, 18 in
+    // two halves; the halves fill the GPU better for fewer rows: 9216 x 2304 8.7 and 8.0.
+    if (a.T > 32 && mx4_best<XT, 4>(a, &rb4) < two) return launch_tt<XT, 4>(a, rb4, s);
+  }
+  return launch_tt<XT, 2>(a, rb, s);
 }
 
 // ------------------------------------------------------------------ weights

@@ -75,6 +75,7 @@ sffn_status_t check_mx4(int32_t N, int32_t K) {
   if (N < 0) return invalid("N must not be negative");
   if (K < 1) return invalid("K must be positive");
   if (K > 1 << 30) return unsupported("K must be at most 2^30");
+  if (N > 1 << 26) return unsupported("N must be at most 2^26");  // 2^32 threads a launch
   const Mx4Dims d = mx4_dims(N, K);
   if ((int64_t)d.nb * d.kb >= (int64_t)1 << 25) return unsupported("N * K must be below 2^36");
   return SFFN_OK;
@@ -245,9 +246,9 @@ sffn_status_t sffn_adamw_step(const sffn_adamw_tensor_t* tensors, int32_t n_tens
   tab.inv_root_correction = (float)(1.0 / std::sqrt(1.0 - std::pow(hp.beta2, (double)hp.step)));
   tab.eps = (float)hp.eps;
   tab.grad_scale = grad_scale;
-  // A launch takes up to ADAMW_TENSORS tensors and MAX_GROUPS workgroups (2^32 - 1 threads);
-  // a longer tensor is cut into parts of whole chunks.
-  constexpr int64_t MAX_GROUPS = (int64_t)1 << 23;
+  // A launch takes up to ADAMW_TENSORS tensors and MAX_GROUPS workgroups (half of the 2^32
+  // threads that a launch must stay below); a longer tensor is cut into parts of whole chunks.
+  constexpr int64_t MAX_GROUPS = ((int64_t)1 << 31) / (ADAMW_CHUNK / 4);
   hipStream_t s = static_cast<hipStream_t>(stream);
   int used = 0;
   int64_t groups = 0;

@@ -4,7 +4,8 @@ RMS norm with the residual's sum and its gradient, products with 4-bit weights, 
 Argument marshalling only, as in ``sparse_ffn``: every step runs in the library's HIP kernels;
 PyTorch supplies device memory and the stream.  With ``stream=None`` a call runs on PyTorch's
 current stream of the tensors' device; a given ``stream`` is used for the kernels and for what
-the call allocates (inputs made on another stream have to be ready on it: the caller's events).
+the call allocates.  Tensors made on another stream have to be ready on it (the caller's events);
+their memory is not given away before the call's work is done.
 """
 from __future__ import annotations
 
@@ -103,8 +104,9 @@ def _elsewhere(f, device, stream):
 
 
 @contextlib.contextmanager
-def _on(device, stream):
-    """Makes `device`, and `stream` if given, current: what the call allocates belongs to it."""
+def _on(device, stream, *tensors):
+    """Makes `device`, and `stream` if given, current: what the call allocates belongs to it, and
+    the memory of its `tensors` stays theirs until the stream is past the call."""
     import torch
     if device.type != "cuda":
         raise ValueError("device tensors are needed")
@@ -116,6 +118,9 @@ def _on(device, stream):
             raise ValueError("stream is not of the tensors' device")
         with torch.cuda.stream(stream):
             yield
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _matrix(t, name, dtype, shape, device):
@@ -146,7 +151,7 @@ def _norm(fn, fp8, x, gain, residual, eps, y, stat, h, stream):
     torch = f.torch
     dev, dt = x.device, x.dtype
     if _elsewhere(f, dev, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, x, gain, residual, y, stat, h):
             return _norm(fn, fp8, x, gain, residual, eps, y, stat, h, None)
     shape = x.shape
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
@@ -206,7 +211,7 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
     torch = f.torch
     dev, dt = h.device, h.dtype
     if _elsewhere(f, dev, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, dy, h, gain, rstd, dres, dx, dgain):
             return rms_norm_backward(dy, h, gain, rstd, dres, with_dgain, dx, dgain)
     shape = h.shape
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
@@ -255,7 +260,7 @@ def mx4_quantize(W, stream=None):
     f = _lib()
     torch = f.torch
     if _elsewhere(f, W.device, stream):
-        with _on(W.device, stream):
+        with _on(W.device, stream, W):
             return mx4_quantize(W)
     if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("W must be a float32 or bfloat16 tensor [N, K]")
@@ -276,7 +281,8 @@ class Mx4Linear:
 
     codes and scales are as mx4_quantize gives them (MXFP4: e2m1 values, one power of two per 32
     columns); in_features is K where it is not 32 * scales.shape[1].  They are laid out once for
-    the kernel, here, and not kept.  bias [N] float32 is borrowed (kept referenced)."""
+    the kernel, here (a call on another stream has to wait for that), and not kept.  bias [N]
+    float32 is borrowed (kept referenced)."""
 
     def __init__(self, codes, scales, bias=None, relu=False, in_features=None, stream=None):
         f = _lib()
@@ -296,7 +302,7 @@ class Mx4Linear:
         st = f.sffn_mx4_bytes(N, K, ctypes.byref(n))
         if st:
             _fail(st, "sffn_mx4_bytes")
-        with _on(dev, stream):
+        with _on(dev, stream, codes, scales):
             tiled = torch.empty(n.value, dtype=torch.uint8, device=dev)
             st = f.sffn_mx4_tile(codes.data_ptr(), scales.data_ptr(), N, K, tiled.data_ptr(),
                                  f.stream(dev.index))
@@ -320,7 +326,7 @@ class Mx4Linear:
         torch = f.torch
         N, K, dev = self.out_features, self.in_features, self.device
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream):
+            with _on(dev, stream, x, x_scale, y, self.tiled, self.bias):
                 return self(x, x_scale, dtype, y)
         shape = x.shape
         xc = f.code.get(x.dtype)
@@ -359,7 +365,9 @@ class AdamW:
     the root of the second as float8_e4m3fn with one float32 scale per 256 elements.  `state`
     continues from given tensors instead of zeros: [m, v] or [m, m_scale, r, r_scale], each a
     list like params; with it, state_bits goes by its length, and `step` is the number of steps
-    done.  The state tensors are in `.state`, in that order."""
+    done.  The state tensors are in `.state`, in that order.  lr, betas, eps and weight_decay may be
+    changed between steps; a step recorded in a graph replays with those it was recorded with,
+    its number among them."""
 
     def __init__(self, params, master=None, state_bits=32, state=None, lr=1e-3,
                  betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=0):
@@ -373,6 +381,9 @@ class AdamW:
             raise ValueError("parameters must be float32 or bfloat16 device tensors")
         for p in self.params:
             _plain(p, "a parameter", dt, p.shape, dev)
+        used = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(used)) < len(used):
+            raise ValueError("a parameter is given twice")
         self.master = None if master is None else list(master)
         if self.master is not None and dt != torch.bfloat16:
             raise ValueError("a master copy needs bfloat16 parameters")
@@ -428,7 +439,8 @@ class AdamW:
         torch = f.torch
         dev = self.device
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream):
+            lists = [self.params, grads, self.master or [], *self.state]
+            with _on(dev, stream, grad_scale, *(t for k in lists for t in k)):
                 return self.step(grads, grad_scale)
         if len(grads) != len(self.params):
             raise ValueError("one gradient for each parameter is needed")

@@ -13,7 +13,9 @@
  *   - No output may overlap an input, except where a call says that it updates in place, and
  *     rms_norm's h, which may be x or the residual itself (same address and stride).
  *   - Non-finite values follow the formulas: they reach the outputs that depend on them.
- *   - Results do not depend on timing: no call adds with atomics. */
+ *   - Results do not depend on timing: no call adds with atomics.
+ *   - Kernel names for sffn_profile_read: rms_norm, rms_norm_fp8, rms_norm_grad,
+ *     rms_norm_grad_sum, mx4_quantize, mx4_tile, mx4_linear, adamw. */
 #ifndef FFN_OPS_H_
 #define FFN_OPS_H_
 
@@ -98,8 +100,9 @@ sffn_status_t sffn_mx4_tile(const uint8_t *codes, const uint8_t *scales, int32_t
  * x [T, K] is SFFN_BF16, SFFN_F32 or SFFN_E4M3; x_scale [T] fp32 multiplies a token's results
  * (required for SFFN_E4M3, otherwise it may be NULL).  bias [N] fp32 may be NULL.  act is
  * max(., 0) if relu is nonzero (NaN stays).  y [T, N] (stride N) is SFFN_F32 or SFFN_BF16.
- * Products are exact, sums in fp32.  Every T is accepted; the kernel is made for T <= 64, and
- * reads the weights again for every further 64 tokens. */
+ * Products are exact, sums in fp32.  N up to 2^26, K up to 2^30, N K below 2^36.  Every T up to
+ * 2^20 is accepted; the kernel is made
+ * for T <= 64, and reads the weights again for every further 64 tokens. */
 sffn_status_t sffn_mx4_linear(const void *tiled, int32_t N, int32_t K, int32_t x_dtype,
                               const void *x, int64_t x_stride, const float *x_scale, int32_t T,
                               const float *bias, int32_t relu, int32_t y_dtype, void *y,

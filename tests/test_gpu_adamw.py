@@ -223,6 +223,7 @@ def test_refusals():
         lambda: sffn.AdamW([p.half()]),
         lambda: sffn.AdamW([p.cpu()]),
         lambda: sffn.AdamW([p, b]),
+        lambda: sffn.AdamW([p, p]),
         lambda: sffn.AdamW([p], master=[p]),
         lambda: sffn.AdamW([b], master=[p[:10]]),
         lambda: sffn.AdamW([p], state_bits=16),

@@ -94,7 +94,7 @@ def test_norm_workspace(ops):
 @pytest.mark.parametrize("kw,status", [
     ({"T": 0}, OK), ({"N": 0}, OK), ({"N": -1}, INVALID), ({"K": 0}, INVALID), ({"T": -1}, INVALID),
     ({"T": (1 << 20) + 1}, UNSUPPORTED), ({"N": 1 << 30, "K": 1 << 20}, UNSUPPORTED),
-    ({"K": (1 << 30) + 1, "N": 1}, UNSUPPORTED), ({"x_dtype": 3}, INVALID), ({"y_dtype": E4M3}, INVALID),
+    ({"K": (1 << 30) + 1, "N": 1}, UNSUPPORTED), ({"N": (1 << 26) + 1, "K": 1}, UNSUPPORTED), ({"x_dtype": 3}, INVALID), ({"y_dtype": E4M3}, INVALID),
     ({"x_dtype": E4M3, "x_scale": None}, INVALID), ({"tiled": None}, INVALID), ({"tiled": A + 8}, INVALID),
     ({"x": None}, INVALID), ({"x_stride": 63}, INVALID), ({"y": None}, INVALID), ({"y": A + 1}, INVALID),
     ({"bias": A + 2}, INVALID), ({"x": A + 1}, INVALID),
