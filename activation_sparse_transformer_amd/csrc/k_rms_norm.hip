@@ -124,7 +124,7 @@ hipError_t launch_t(const NormArgs& a, hipStream_t s) {
     b.y = static_cast<char*>(a.y) + r * a.d * (FP8 ? 1 : (int64_t)sizeof(T));
     if (a.stat) b.stat = a.stat + r;
     if (a.h) b.h = static_cast<T*>(a.h) + r * a.d;
-    const hipError_t e = norm_shape(a.d, [&](auto lanes, auto nv) {
+    const hipError_t e = norm_shape<false>(a.d, [&](auto lanes, auto nv) {
       constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
       constexpr int RPB = L < 256 ? 256 / L : 1;
       rms_norm_kernel<T, G, NV, L, FP8>

@@ -7,7 +7,8 @@
 // dgain in registers too; a workgroup joins its row groups in LDS in a fixed order and writes
 // one partial row, and a second kernel adds the partial rows in order (no atomics: the result
 // depends on the sizes alone).  Bound by memory: 16384 x 2304 bf16 with dres moves 302 MB in
-// 58 us (5.2 TB/s), the second kernel takes 3.
+// 57 us (5.3 TB/s), the second kernel takes 3.  (Loading a lane's next row before this one is
+// reduced helped 8192 x 4096 by 3 us and cost 16384 x 2304 as much.)
 #include "ops_common.hpp"
 
 namespace sffn {
@@ -143,7 +144,7 @@ constexpr int norm_grad_threads(int L) { return L < 256 ? 256 : L; }
 
 template <typename T, typename G>
 hipError_t launch_t(const NormGradArgs& a, hipStream_t s) {
-  return norm_shape(a.d, [&](auto lanes, auto nv) {
+  return norm_shape<true>(a.d, [&](auto lanes, auto nv) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value, B = norm_grad_threads(L);
     rms_norm_grad_kernel<T, G, NV, L, B>
         <<<dim3((unsigned)norm_grad_groups(a.rows, a.d)), dim3(B), 0, s>>>(a);
@@ -154,11 +155,11 @@ hipError_t launch_t(const NormGradArgs& a, hipStream_t s) {
 }  // namespace
 
 // Each workgroup's partial row costs a write and a read, so there are only as many as keep the
-// memory busy (16384 x 2304: 512 take 61.4 us, 768 63.0, 384 73.1), with equal numbers of rows,
+// memory busy (16384 x 2304: 512 take 59.8 us, 768 63.4, 384 67.9), with equal numbers of rows,
 // and at least two rows each once there is a half CU's worth (333 x 1537: 167 7.2 us, 333 7.6).
 int norm_grad_groups(int64_t rows, int32_t d) {
-  const int L = norm_lanes(d), rpb = norm_grad_threads(L) / L;
-  const int64_t need = (rows + rpb - 1) / rpb, most = L > 256 ? 256 : 512;
+  const int L = norm_lanes(d, true), rpb = norm_grad_threads(L) / L;
+  const int64_t need = (rows + rpb - 1) / rpb, most = L > 512 ? 256 : 512;
   int64_t turns = (need + most - 1) / most;
   if (turns == 1 && need > 128) turns = 2;
   return turns > 0 ? (int)((need + turns - 1) / turns) : 0;

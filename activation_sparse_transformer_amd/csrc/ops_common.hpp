@@ -157,8 +157,15 @@ __device__ __forceinline__ float inv_rms(float ms) { return 1.f / sqrtf(ms); }
 // Lanes that share a row of d elements in the norm kernels; a lane keeps 8, 16, or (16 waves)
 // up to 32 of them.  Few elements a lane leave registers for many rows in flight: 8192 x 4096
 // takes 46 us with 4 waves a row and 51 with one (gradient 54 and 69), 16384 x 1024 27 and 25.
-inline int norm_lanes(int32_t d) {
-  return d <= 128 ? 16 : d <= 256 ? 32 : d <= 1024 ? 64 : d <= 4096 ? 256 : 1024;
+// The gradient, with more to keep, takes 8 waves above 2048 (16384 x 2304: 59.8 us, 61.5 with 4;
+// the norm itself 60 and 49 with 8 bits out).
+inline int norm_lanes(int32_t d, bool grad) {
+  return d <= 128    ? 16
+         : d <= 256  ? 32
+         : d <= 1024 ? 64
+         : d <= 2048 ? 256
+         : d <= 4096 ? (grad ? 512 : 256)
+                     : 1024;
 }
 struct NormArgs {
   const void* x;
@@ -174,9 +181,9 @@ struct NormArgs {
   void* h;
 };
 // Calls f(lanes, vectors of 8 a lane) with both as integral constants, for a row of d elements.
-template <typename F>
+template <bool GRAD, typename F>
 hipError_t norm_shape(int32_t d, F&& f) {
-  const int L = norm_lanes(d), nv = (d + 8 * L - 1) / (8 * L);
+  const int L = norm_lanes(d, GRAD), nv = (d + 8 * L - 1) / (8 * L);
 #define SFFN_SHAPE(l, n) \
   if (L == l && nv == n) return f(std::integral_constant<int, l>(), std::integral_constant<int, n>())
   SFFN_SHAPE(16, 1);
@@ -184,7 +191,11 @@ hipError_t norm_shape(int32_t d, F&& f) {
   SFFN_SHAPE(64, 1);
   SFFN_SHAPE(64, 2);
   SFFN_SHAPE(256, 1);
-  SFFN_SHAPE(256, 2);
+  if constexpr (GRAD) {
+    SFFN_SHAPE(512, 1);
+  } else {
+    SFFN_SHAPE(256, 2);
+  }
   SFFN_SHAPE(1024, 1);
   SFFN_SHAPE(1024, 2);
   SFFN_SHAPE(1024, 3);
