@@ -16,45 +16,7 @@
 namespace sffn {
 namespace {
 
-// Four consecutive elements.  NT: past the caches.
-template <bool NT, typename V, typename M>
-__device__ __forceinline__ V load_v(const M* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
-  else return *p;
-}
-template <bool NT, typename V, typename M>
-__device__ __forceinline__ void store_v(M* p, V v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
-  else *p = v;
-}
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef uint32_t u32_a1 __attribute__((aligned(1)));
-
-template <bool NT>
-__device__ __forceinline__ void load4(const float* p, int n, float* o) {
-  if (n >= 4) {
-    const f32x4 v = load_v<NT, f32x4>(reinterpret_cast<const f32x4_a4*>(p));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = i < n ? p[i] : 0.f;
-  }
-}
-template <bool NT>
-__device__ __forceinline__ void load4(const uint16_t* p, int n, float* o) {
-  u32x2 v = u32x2{0, 0};
-  if (n >= 4) {
-    v = load_v<NT, u32x2>(reinterpret_cast<const u32x2_a2*>(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = __uint_as_float((i & 1) ? (v[i >> 1] & 0xffff0000u) : (v[i >> 1] << 16));
-}
+// Four consecutive elements, of which the first n exist.  NT: past the caches.
 template <bool NT>
 __device__ __forceinline__ void store4(float* p, const float* v, int n) {
   if (n >= 4) {

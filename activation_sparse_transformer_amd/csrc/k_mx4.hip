@@ -16,7 +16,6 @@
 namespace sffn {
 namespace {
 
-typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
@@ -170,7 +169,6 @@ __device__ __forceinline__ void mx4_store(const Mx4Args& a, f32x4 s, int tok, in
   if (a.y_bf16) {
     uint16_t* y = static_cast<uint16_t*>(a.y) + at;
     if (n + 4 <= N) {
-      typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
       *reinterpret_cast<u32x2_a2*>(y) =
           u32x2{(uint32_t)f32_to_bf16(o[0]) | ((uint32_t)f32_to_bf16(o[1]) << 16),
                 (uint32_t)f32_to_bf16(o[2]) | ((uint32_t)f32_to_bf16(o[3]) << 16)};

@@ -14,9 +14,46 @@
 namespace sffn {
 namespace {
 
-// B threads: B / L rows at a time.
+// dgain of grad_columns(B) columns over all rows, by the B threads of a workgroup: 64 row groups
+// of lanes of 4 columns, joined in order.
+constexpr int grad_columns(int B) { return B / 16; }
+template <typename T, int B>
+__device__ __forceinline__ void sum_columns(const NormGradArgs& a, int blk) {
+  constexpr int GROUPS = 64, LANES = B / GROUPS, COLUMNS = grad_columns(B);
+  __shared__ float join[GROUPS][COLUMNS + 1];
+  const int c4 = (int)(threadIdx.x % LANES) * 4, g = (int)(threadIdx.x / LANES);
+  const int col = blk * COLUMNS + c4, n = a.d - col;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t row = g; row < a.rows; row += GROUPS) {
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride + col;
+    const T* h = static_cast<const T*>(a.h) + row * a.h_stride + col;
+    const float rstd = a.rstd[row];
+    float y[4], x[4];
+    load4<false>(dy, n, y);
+    load4<false>(h, n, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += y[i] * (x[i] * rstd);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) join[g][c4 + i] = s[i];
+  __syncthreads();
+  const int c = (int)threadIdx.x;
+  if (c < COLUMNS && blk * COLUMNS + c < a.d) {
+    float t = 0.f;
+#pragma unroll 16
+    for (int i = 0; i < GROUPS; ++i) t += join[i][c];
+    a.dgain[blk * COLUMNS + c] = t;
+  }
+}
+
+// B threads: B / L rows at a time, by row_groups workgroups; the ones past them sum dgain.
 template <typename T, typename G, int NV, int L, int B>
-__global__ __launch_bounds__(B) void rms_norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(B) void rms_norm_grad_kernel(NormGradArgs a, int row_groups) {
+  if ((int)blockIdx.x >= row_groups) {
+    sum_columns<T, B>(a, (int)blockIdx.x - row_groups);
+    return;
+  }
   constexpr int RPB = B / L;
   __shared__ float red[2][L > 64 ? L / 64 : 1];
   __shared__ float join[RPB > 1 ? RPB * 8 * L : 1];
@@ -39,7 +76,7 @@ __global__ __launch_bounds__(B) void rms_norm_grad_kernel(NormGradArgs a) {
   }
   int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+       row += (int64_t)row_groups * RPB, turn ^= 1) {
     const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
     const T* dres = static_cast<const T*>(a.dres) + row * a.dres_stride;
@@ -95,7 +132,7 @@ __global__ __launch_bounds__(B) void rms_norm_grad_kernel(NormGradArgs a) {
       else if (e < d) store8_n(dx + e, o, d - e);
     }
   }
-  if (!a.dgain) return;
+  if (!a.part) return;
   float* part = a.part + (int64_t)blockIdx.x * d;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -142,27 +179,37 @@ __global__ __launch_bounds__(1024) void rms_norm_grad_sum_kernel(const float* pa
 
 constexpr int norm_grad_threads(int L) { return L < 256 ? 256 : L; }
 
+// Whether dgain's columns are summed by further workgroups of the same launch, which read dy and h
+// once more: for few rows that is less than a second launch (333 x 1537 fp32: a call 12.9 us with
+// two).
+bool one_launch(int64_t rows, int32_t d) { return rows <= 1024 && rows * d <= 1 << 20; }
+
+// Each workgroup's partial row costs a write and a read, so there are only as many as keep the
+// memory busy (16384 x 2304: 512 take 59.8 us, 768 63.4, 384 67.9), with equal numbers of rows.
+int row_groups(int64_t rows, int32_t d) {
+  const int L = norm_lanes(d, true), rpb = norm_grad_threads(L) / L;
+  const int64_t need = (rows + rpb - 1) / rpb, most = L > 512 ? 256 : 512;
+  if (one_launch(rows, d)) return (int)need;
+  const int64_t turns = (need + most - 1) / most;
+  return (int)((need + turns - 1) / turns);
+}
+
 template <typename T, typename G>
 hipError_t launch_t(const NormGradArgs& a, hipStream_t s) {
   return norm_shape<true>(a.d, [&](auto lanes, auto nv) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value, B = norm_grad_threads(L);
-    rms_norm_grad_kernel<T, G, NV, L, B>
-        <<<dim3((unsigned)norm_grad_groups(a.rows, a.d)), dim3(B), 0, s>>>(a);
+    const int groups = row_groups(a.rows, a.d),
+              columns = a.dgain && !a.part ? (a.d + grad_columns(B) - 1) / grad_columns(B) : 0;
+    rms_norm_grad_kernel<T, G, NV, L, B><<<dim3((unsigned)(groups + columns)), dim3(B), 0, s>>>(
+        a, groups);
     return hipGetLastError();
   });
 }
 
 }  // namespace
 
-// Each workgroup's partial row costs a write and a read, so there are only as many as keep the
-// memory busy (16384 x 2304: 512 take 59.8 us, 768 63.4, 384 67.9), with equal numbers of rows,
-// and at least two rows each once there is a half CU's worth (333 x 1537: 167 7.2 us, 333 7.6).
 int norm_grad_groups(int64_t rows, int32_t d) {
-  const int L = norm_lanes(d, true), rpb = norm_grad_threads(L) / L;
-  const int64_t need = (rows + rpb - 1) / rpb, most = L > 512 ? 256 : 512;
-  int64_t turns = (need + most - 1) / most;
-  if (turns == 1 && need > 128) turns = 2;
-  return turns > 0 ? (int)((need + turns - 1) / turns) : 0;
+  return one_launch(rows, d) ? 0 : row_groups(rows, d);
 }
 
 hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a, hipStream_t s) {

@@ -130,15 +130,15 @@ sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const vo
     if (misaligned(gain, size_of(gain_dtype)) || misaligned(rstd, 4) ||
         misaligned(dx, size_of(dtype)))
       return invalid("a pointer is not aligned to its element");
-    if (dgain && (!workspace || misaligned(workspace, 16) ||
-                  workspace_bytes < (size_t)groups * d * sizeof(float)))
+    if (dgain && groups > 0 && (!workspace || misaligned(workspace, 16) ||
+                                workspace_bytes < (size_t)groups * d * sizeof(float)))
       return invalid("workspace is NULL, misaligned or too small");
     const NormGradArgs a{dy, dy_stride, h, h_stride, gain, rstd, dres, dres ? dres_stride : 0,
-                         rows, d, dx, dgain, part};
+                         rows, d, dx, dgain, dgain && groups > 0 ? part : nullptr};
     auto f = [&] { return launch_rms_norm_grad(dtype == SFFN_BF16, gain_dtype == SFFN_F32, a, s); };
     OPS_TRY(api_run("rms_norm_grad", s, f));
   }
-  if (!dgain) return SFFN_OK;
+  if (!dgain || (rows > 0 && groups == 0)) return SFFN_OK;
   auto f = [&] { return launch_rms_norm_grad_sum(part, groups, d, dgain, s); };
   return api_run("rms_norm_grad_sum", s, f);
 }

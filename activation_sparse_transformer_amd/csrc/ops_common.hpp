@@ -18,7 +18,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 // The same types at an element's alignment: global memory takes vector accesses at any
 // address, so rows that start off a 16-byte boundary need no path of their own.
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
@@ -80,6 +82,44 @@ __device__ __forceinline__ void store8_n(T* p, const float* v, int n) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) store1(p + i, v[i]);
+}
+
+// One vector access; NT: past the caches.
+template <bool NT, typename V, typename M>
+__device__ __forceinline__ V load_v(const M* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else return *p;
+}
+template <bool NT, typename V, typename M>
+__device__ __forceinline__ void store_v(M* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+  else *p = v;
+}
+// Four consecutive elements, of which the first n exist.
+template <bool NT>
+__device__ __forceinline__ void load4(const float* p, int n, float* o) {
+  if (n >= 4) {
+    const f32x4 v = load_v<NT, f32x4>(reinterpret_cast<const f32x4_a4*>(p));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = i < n ? p[i] : 0.f;
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void load4(const uint16_t* p, int n, float* o) {
+  u32x2 v = u32x2{0, 0};
+  if (n >= 4) {
+    v = load_v<NT, u32x2>(reinterpret_cast<const u32x2_a2*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = __uint_as_float((i & 1) ? (v[i >> 1] & 0xffff0000u) : (v[i >> 1] << 16));
 }
 
 // Four / eight values to e4m3, to nearest-even.  |v| <= 448 up to rounding, or NaN.
@@ -218,8 +258,10 @@ struct NormGradArgs {
   int32_t d;
   void* dx;
   float* dgain;
-  float* part;  // [norm_grad_groups(rows, d), d] partial sums of dgain
+  float* part;  // [norm_grad_groups(rows, d), d] partial sums of dgain, or null
 };
+// Partial rows of dgain, whose sum takes a second kernel; 0 where the first one's further
+// workgroups sum dgain themselves.
 int norm_grad_groups(int64_t rows, int32_t d);
 hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a, hipStream_t s);
 // dgain[c] = sum of the n partial rows (0 with none)

@@ -233,7 +233,8 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
         dgain = torch.empty(d, dtype=torch.float32, device=dev) if dgain is None else \
             _plain(dgain, "dgain", torch.float32, (d,), dev)
         nb = _norm_workspace(rows, d)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        if nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     else:
         dgain = None
     st = f.sffn_rms_norm_backward(f.code[dt], f.code[gain.dtype], dy.data_ptr(), ys,

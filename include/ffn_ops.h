@@ -59,7 +59,8 @@ sffn_status_t sffn_rms_norm_fp8(int32_t dtype, int32_t gain_dtype, const void *x
                                 const void *gain, float eps, int64_t rows, int32_t d, void *q,
                                 float *scale, void *h, void *stream);
 
-/* (host only) Bytes of scratch sffn_rms_norm_backward needs for these sizes (0 with zero rows). */
+/* (host only) Bytes of scratch sffn_rms_norm_backward needs for these sizes with dgain: 0 for few
+ * rows, which are summed without it. */
 sffn_status_t sffn_rms_norm_backward_workspace(int64_t rows, int32_t d, size_t *bytes);
 
 /* Gradient of sffn_rms_norm.  With xh = h * rstd and t = dy * gain:
@@ -68,7 +69,7 @@ sffn_status_t sffn_rms_norm_backward_workspace(int64_t rows, int32_t d, size_t *
  * reaches h past the norm, may be NULL.  dx [rows, d] (stride d, dtype) is the gradient of both
  * x and the residual; dgain [d] is fp32 and may be NULL; with zero rows it is cleared.  dx may be dres
  * itself.  Sums are in fp32 in an order that depends on the sizes alone.  workspace: as many
- * bytes as sffn_rms_norm_backward_workspace says, 16-byte aligned. */
+ * bytes as sffn_rms_norm_backward_workspace says, 16-byte aligned (NULL for 0). */
 sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const void *dy,
                                      int64_t dy_stride, const void *h, int64_t h_stride,
                                      const void *gain, const float *rstd, const void *dres,

@@ -236,7 +236,8 @@ def test_grad_lengths(d, dtype, gain_f32):
 
 
 @pytest.mark.parametrize("rows,d", [(1024, 2048), (5003, 2304), (1500, 1537), (20000, 64), (4100, 200),
-                                    (3001, 2560), (1025, 2561), (300, 20000)])
+                                    (3001, 2560), (1025, 2561), (300, 20000), (1024, 1024), (1024, 1025),
+                                    (1000, 67)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_grad_many_rows(rows, d, dtype):
     torch, sffn = need_gpu()

@@ -65,7 +65,7 @@ def test_norm_fp8_needs_scales(ops):
 
 
 GRAD = dict(dtype=BF16, gain_dtype=F32, dy=A, dy_stride=64, h=A, h_stride=64, gain=A, rstd=A, dres=A,
-            dres_stride=64, rows=2, d=64, dx=A, dgain=A, ws=A, nb=1 << 30)
+            dres_stride=64, rows=5000, d=64, dx=A, dgain=A, ws=A, nb=1 << 30)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -82,12 +82,10 @@ def test_norm_backward_arguments(ops, kw, status):
 
 def test_norm_workspace(ops):
     f, n = ops._lib(), ctypes.c_size_t()
-    prev = 0
     for rows in (0, 1, 4, 1000, 100000, 1 << 30):
         assert f.sffn_rms_norm_backward_workspace(rows, 2048, ctypes.byref(n)) == OK
         assert n.value % (2048 * 4) == 0 and n.value <= 1024 * 2048 * 4
-        assert (n.value == 0) == (rows == 0)
-        prev = max(prev, n.value)
+        assert (n.value == 0) == (rows <= 4)  # few rows are summed in the same launch
     assert f.sffn_rms_norm_backward_workspace(4, 2048, None) == INVALID
 
 
