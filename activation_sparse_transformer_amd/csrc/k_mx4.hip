@@ -362,8 +362,9 @@ hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
 // Estimated time of a tile shape, in units of a wave's work on one block of 16 rows, 128 columns
 // and up to 32 tokens: per block of columns that on the tokens (loads, conversions) and on RB
 // blocks of weights, for as many workgroups as a CU gets, and for every workgroup (for every
-// two where two fit at once) the 10 units, 2 us, that its loads and its join take to pass.  Four
-// tiles of tokens cost 1.7 times two (the weights are expanded once) and 16 units.  Fitted to sweeps of RB and
+// two where two fit at once) the 10 units, 2 us, that its loads and its join take to pass.  Three
+// and four tiles of tokens cost 1.35 and 1.7 times two (the weights are expanded once), and 13 and
+// 16 units.  Fitted to sweeps of RB and
 // TT over N 2048 .. 65536, K 256 .. 8192.
 template <int XT, int TT, int RB>
 double mx4_cost(const Mx4Args& a) {
@@ -371,7 +372,9 @@ double mx4_cost(const Mx4Args& a) {
   const int64_t groups = (a.d.nb * mx4_token_groups(a, TT) + RB - 1) / RB, n = (groups + 255) / 256;
   const int64_t turns = mx4_pairs<XT, TT, RB>() ? (n + 1) / 2 : n;
   const double blocks = a.d.kb > MX4_WAVES ? (double)a.d.kb / MX4_WAVES : 1.0;
-  return (TT == 4 ? 16.0 : 10.0) * (double)turns + (double)n * blocks * (tokens + RB) * (TT == 4 ? 1.7 : 1.0);
+  const double more = TT > 2 ? TT - 2 : 0;
+  return (10.0 + 3.0 * more) * (double)turns +
+         (double)n * blocks * (tokens + RB) * (1.0 + 0.35 * more);
 }
 template <int XT, int TT>
 double mx4_best(const Mx4Args& a, int* rb) {
@@ -398,16 +401,20 @@ hipError_t launch_tt(const Mx4Args& a, int rb, hipStream_t s) {
 
 template <int XT>
 hipError_t launch_x(const Mx4Args& a, hipStream_t s) {
-  int rb = 1, rb4 = 1;
+  int rb = 1, rb_all = 1;
   if (a.T <= 16) {
     mx4_best<XT, 1>(a, &rb);
     return launch_tt<XT, 1>(a, rb, s);
   }
   const double two = mx4_best<XT, 2>(a, &rb);
-  if constexpr (XT != SFFN_F32) {  // (four tiles of fp32 tokens would not fit the LDS)
-    // 64 tokens at once read and expand the weights once: 32768 x 2048 in 8 bits 16 us, 18 in
-    // two halves; the halves fill the GPU better for fewer rows: 9216 x 2304 8.7 and 8.0.
-    if (a.T > 32 && mx4_best<XT, 4>(a, &rb4) < two) return launch_tt<XT, 4>(a, rb4, s);
+  if constexpr (XT != SFFN_F32) {  // (more than two tiles of fp32 tokens would not fit the LDS)
+    // All tokens at once read and expand the weights once: 32768 x 2048 with 64 in 8 bits 16 us, 18
+    // in two halves; the halves fill the GPU better for fewer rows: 9216 x 2304 8.7 and 8.0.
+    if (a.T > 48) {
+      if (mx4_best<XT, 4>(a, &rb_all) < two) return launch_tt<XT, 4>(a, rb_all, s);
+    } else if (a.T > 32) {
+      if (mx4_best<XT, 3>(a, &rb_all) < two) return launch_tt<XT, 3>(a, rb_all, s);
+    }
   }
   return launch_tt<XT, 2>(a, rb, s);
 }
