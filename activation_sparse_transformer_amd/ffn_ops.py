@@ -77,9 +77,9 @@ def _lib():
             fn.restype = ctypes.c_int
             setattr(f, name, fn)
         f.torch = torch
-        f.current_device = torch.cuda.current_device
-        # the current stream's handle of a device index (without making a Stream object, where
-        # this torch has the call)
+        # the current device's index, and the handle of a device's current stream (without making
+        # a Stream object): torch's own quick forms, where it has them
+        f.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         f.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
         f.code = {torch.float32: _base.SFFN_F32, torch.bfloat16: _base.SFFN_BF16,
@@ -98,9 +98,10 @@ def _fail(status, where):
 
 def _elsewhere(f, device, stream):
     """Whether a call has to enter `_on` first: a stream is given, or `device` is not current."""
-    if device.index is None:
+    i = device.index
+    if i is None:
         raise ValueError("device tensors are needed")
-    return stream is not None or device.index != f.current_device()
+    return stream is not None or i != f.current_device()
 
 
 @contextlib.contextmanager
@@ -125,8 +126,10 @@ def _on(device, stream, *tensors):
 
 def _matrix(t, name, dtype, shape, device):
     """Row stride of a [rows, d] tensor whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on {device}")
+    if t.is_contiguous():
+        return shape[1]
     s = t.stride()
     if shape[1] > 1 and s[1] != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
@@ -136,7 +139,8 @@ def _matrix(t, name, dtype, shape, device):
 
 
 def _plain(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() \
+            or t.get_device() != device.index:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} "
                          f"on {device}")
     return t
@@ -157,7 +161,7 @@ def _norm(fn, fp8, x, gain, residual, eps, y, stat, h, stream):
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
         raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
     rows, d = shape
-    xs = _matrix(x, "x", dt, shape, dev)
+    xs = d if x.is_contiguous() else _matrix(x, "x", dt, shape, dev)
     rs = _matrix(residual, "residual", dt, shape, dev) if residual is not None else 0
     if gain.dtype != dt and gain.dtype != torch.float32:
         raise ValueError("gain must have x's type or float32")
@@ -217,7 +221,7 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
         raise ValueError("h must be a float32 or bfloat16 tensor [rows, d]")
     rows, d = shape
-    hs = _matrix(h, "h", dt, shape, dev)
+    hs = d if h.is_contiguous() else _matrix(h, "h", dt, shape, dev)
     ys = _matrix(dy, "dy", dt, shape, dev)
     rs = _matrix(dres, "dres", dt, shape, dev) if dres is not None else 0
     if gain.dtype != dt and gain.dtype != torch.float32:
