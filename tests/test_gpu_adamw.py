@@ -149,6 +149,25 @@ def test_large_tensor_and_continued_state():
         _step_and_check(torch, again, [g * 0.5 for g in grads], None, HYPER)
 
 
+def test_offsets_beyond_32_bits():
+    """A tensor of more than 2^31 elements: its last blocks take the step of a small tensor."""
+    torch, sffn = need_gpu()
+    n, tail = (1 << 31) + 256 + 77, 256 + 77  # the tail starts at a block
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    p[-tail:] = torch.randn(tail, device="cuda").to(torch.bfloat16)
+    g[-tail:] = torch.randn(tail, device="cuda").to(torch.bfloat16)
+    small, sg = p[-tail:].clone(), g[-tail:].clone()
+    opt = sffn.AdamW([p], state_bits=8, **HYPER)
+    ref = sffn.AdamW([small], state_bits=8, **HYPER)
+    for _ in range(2):
+        opt.step([g])
+        ref.step([sg])
+    assert torch.equal(p[-tail:], small) and not p[:-tail].any()
+    for k, count in zip(range(4), (tail, 2, tail, 2)):
+        assert torch.equal(opt.state[k][0][-count:].float(), ref.state[k][0].float())
+
+
 def test_matrix_parameters_and_late_steps():
     torch, sffn = need_gpu()
     hyper = dict(lr=3e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0)

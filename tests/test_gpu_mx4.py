@@ -158,6 +158,26 @@ def test_layout_of_tokens():
     assert torch.equal(lin(far), lin(x))
 
 
+def test_weights_beyond_32_bits():
+    """A layout of more than 2^31 bytes: its last rows give what they give alone."""
+    torch, sffn = need_gpu()
+    N, K, last = (1 << 22) + 9, 1024, 25
+    rng = np.random.default_rng(5)
+    codes, scales = _weights(rng, last, K)
+    big = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    sc = torch.full((N, K // 32), 120, dtype=torch.uint8, device="cuda")
+    big[-last:], sc[-last:] = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    lin = sffn.Mx4Linear(big, sc)
+    assert lin.tiled.numel() > 1 << 31
+    del big, sc
+    x = torch.from_numpy(rng.standard_normal((2, K)).astype(np.float32)).cuda().to(torch.bfloat16)
+    y = lin(x, dtype=torch.float32)
+    z = x.float().cpu().double().numpy() @ _decode(codes, scales, K).T
+    size = np.abs(x.float().cpu().double().numpy()) @ np.abs(_decode(codes, scales, K)).T
+    assert np.all(np.abs(y[:, -last:].cpu().double().numpy() - z) <= (K + 20) * 2.0 ** -23 * size + 1e-30)
+    assert not y[:, :-last].any()
+
+
 def test_empty_and_streams():
     torch, sffn = need_gpu()
     rng = np.random.default_rng(3)

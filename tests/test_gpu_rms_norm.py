@@ -135,6 +135,24 @@ def test_norm_in_place_and_given_outputs():
     a, b, c = sffn.rms_norm(x, gain, residual=stream, h=stream, y=y, rstd=rstd)
     assert a is y and b is stream and c is rstd
     assert torch.equal(y, y0) and torch.equal(stream, h0) and torch.equal(rstd, r0)
+    own = x.clone()
+    _, h, _ = sffn.rms_norm(own, gain, residual=res, h=own)
+    assert h is own and torch.equal(own, h0)
+
+
+def test_norm_more_rows_than_one_launch_takes():
+    torch, sffn = need_gpu()
+    rows = (1 << 21) + 37
+    x = torch.randn((rows, 8), device="cuda").to(torch.bfloat16)
+    gain = torch.ones(8, dtype=torch.bfloat16, device="cuda")
+    y, h, rstd = sffn.rms_norm(x, gain, residual=x)
+    for at in (slice(0, 64), slice((1 << 21) - 40, (1 << 21) + 37)):
+        part = x[at].contiguous()
+        y2, h2, r2 = sffn.rms_norm(part, gain, residual=part)
+        assert torch.equal(y[at], y2) and torch.equal(h[at], h2) and torch.equal(rstd[at], r2)
+    q, s, _ = sffn.rms_norm_fp8(x, gain)
+    q2, s2, _ = sffn.rms_norm_fp8(x[-50:].contiguous(), gain)
+    assert torch.equal(q[-50:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-50:], s2)
 
 
 def test_norm_unaligned_and_repeatable():
