@@ -10,7 +10,8 @@
 // sums over 128 columns came out up to 1e-4 of the absolute products off; these are fp32.)
 // The waves of a workgroup split k and add their fp32 sums in LDS in wave order.
 //
-// Bound by reading the weights at few tokens: 65536 x 8192 at 4 tokens 49.8 us (5.7 TB/s).
+// Bound by reading the weights at few tokens: 65536 x 8192 at 4 tokens 50.2 us (5.7 TB/s); at 64
+// tokens and many rows by expansion and products (65536 x 2048 bf16 31 us, e4m3 28).
 #include "ops_common.hpp"
 
 namespace sffn {
@@ -112,8 +113,8 @@ struct Tok8<SFFN_F32> {
 // 16 tokens x 128 columns on their way to the matrix cores.  A product wants lane (q, r) to hold
 // token r, so its own loads would touch 16 rows in every group of 16 lanes, which costs four
 // times a contiguous load: a wave loads whole rows instead (LPR lanes a row) and turns them in
-// its own piece of LDS.  16-byte units are permuted within a row (by the token) so that neither
-// side conflicts.
+// its own piece of LDS.  16-byte units are permuted within a row (by the token) so that the reads
+// of 16 rows meet in no bank (the 8-byte ones of e4m3 still do in pairs; it costs no time).
 template <int XT>
 struct TokTile {
   typedef typename Tok8<XT>::elem E;
@@ -133,7 +134,9 @@ struct TokTile {
       v[i] = *reinterpret_cast<const u32x4_a1*>(p);
     }
   }
-  static __device__ __forceinline__ int unit(int t, int u) { return t * LPR + (u ^ (t & (LPR < 16 ? LPR - 1 : 15))); }
+  static __device__ __forceinline__ int unit(int t, int u) {
+    return t * LPR + (u ^ (t & (LPR < 16 ? LPR - 1 : 15)));
+  }
   __device__ __forceinline__ void put(u32x4* lds, int lane) const {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) lds[unit(i * RPL + lane / LPR, lane % LPR)] = v[i];
@@ -245,12 +248,13 @@ constexpr bool mx4_pairs() {
 // its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048).
 // Many waves hide the loads: a second block of columns in flight in a wave gained nothing.
 template <int XT, int TT, int RB, int KS>
-__global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs<XT, TT, RB>() ? 4 : 2)) void mx4_linear_kernel(Mx4Args a) {
+__global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs<XT, TT, RB>() ? 4 : 2)) void
+mx4_linear_kernel(Mx4Args a) {
   typedef TokTile<XT> Tile;
   typedef typename Tile::E E;
   constexpr bool TURN = TT > 1;
   constexpr int UNITS = TURN ? TT * Tile::BYTES / 16 : 0;  // of a wave's tokens
-  constexpr int PART = RB * TT * 64;            // of a wave's sums
+  constexpr int PART = RB * TT * 64;                       // of a wave's sums
   __shared__ u32x4 lds[MX4_WAVES * (UNITS > PART ? UNITS : PART)];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int q = lane >> 4, r = lane & 15;
@@ -364,8 +368,7 @@ hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
 // blocks of weights, for as many workgroups as a CU gets, and for every workgroup (for every
 // two where two fit at once) the 10 units, 2 us, that its loads and its join take to pass.  Three
 // and four tiles of tokens cost 1.35 and 1.7 times two (the weights are expanded once), and 13 and
-// 16 units.  Fitted to sweeps of RB and
-// TT over N 2048 .. 65536, K 256 .. 8192.
+// 16 units.  Fitted to sweeps of RB and TT over N 2048 .. 65536, K 256 .. 8192.
 template <int XT, int TT, int RB>
 double mx4_cost(const Mx4Args& a) {
   const double tokens = XT == SFFN_F32 ? 4.0 : TT == 1 ? 2.2 : XT == SFFN_BF16 ? 3.0 : 1.5;
