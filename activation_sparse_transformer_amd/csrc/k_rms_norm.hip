@@ -90,14 +90,13 @@ __global__ __launch_bounds__(L > 256 ? 1024 : 256) void rms_norm_kernel(NormArgs
     big = row_reduce<L>(big, MaxNan(), red[1]);
     const float t = big / E4M3_MAX;
     stat = t < SCALE_MIN ? SCALE_MIN : t;
-    const float inv = 1.f / stat;
+    const Quotients over(stat);
     uint8_t* q = static_cast<uint8_t*>(a.y) + row * d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int e = (v * L + li) * 8;
       if (e >= d) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] *= inv;
+      over(h[v]);
       store_e4m3x8(q + e, h[v], d - e);
     }
   } else {

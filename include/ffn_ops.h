@@ -51,8 +51,8 @@ sffn_status_t sffn_rms_norm(int32_t dtype, int32_t gain_dtype, const void *x, in
                             void *stream);
 
 /* The same norm with its output in 8 bits and one scale a row, the form sffn_mx4_linear takes:
- *   scale = max(max_i |y_i| / 448, 2^-126),  q = e4m3(y / scale)  (to nearest-even)
- * q [rows, d] bytes, scale [rows] fp32.  A row of zeros gives zeros; a NaN or an infinity in a
+ *   scale = max(max_i |y_i| / 448, 2^-126),  q = e4m3(y / scale)
+ * (the quotient rounded to fp32, then to nearest-even).  q [rows, d] bytes, scale [rows] fp32.  A row of zeros gives zeros; a NaN or an infinity in a
  * row gives a scale that is not finite. */
 sffn_status_t sffn_rms_norm_fp8(int32_t dtype, int32_t gain_dtype, const void *x,
                                 int64_t x_stride, const void *residual, int64_t residual_stride,

@@ -347,3 +347,38 @@ def test_norm_refusals():
     with pytest.raises(sffn.SffnError) as ei:
         sffn.rms_norm(wide, torch.ones(32769, device="cuda"))
     assert ei.value.status == sffn.SFFN_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ 8-bit codes
+
+def _midpoints():
+    """The values half way between neighbours of e4m3 from 2^-6 to 448, as float32."""
+    v = np.array([(1 + m / 8) * 2.0 ** e for e in range(-6, 9) for m in range(8)][:-1])  # (the last one is NaN)
+    return ((v[1:] + v[:-1]) / 2).astype(np.float32)
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -110, 2.0 ** -122, 2.0 ** 100])
+def test_fp8_codes_are_of_the_quotient(size):
+    """q = e4m3(y / scale) with the quotient in fp32, no reciprocal in its place: values of y within
+    a few roundings of the middle between two codes take the code of the quotient.  The gain
+    brings every column there without a change to the row's statistics."""
+    torch, sffn = need_gpu()
+    d = 32768
+    rng = np.random.default_rng(11)
+    x = (0.5 + rng.random((1, d))).astype(np.float32)
+    x[0, 0] = 300
+    to = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    y0 = sffn.rms_norm(to(x), torch.ones(d, device="cuda"))[0].cpu().numpy()[0]
+    top = np.float32(y0[0] * np.float32(size))
+    s = max(top / np.float32(448), np.float32(2.0 ** -126))
+    # in double; the sizes are powers of two, so only y0's own digits round here
+    gain = (rng.choice(_midpoints(), d).astype(np.float64) * float(s) / y0).astype(np.float32)
+    gain[0] = size
+    y = sffn.rms_norm(to(x), to(gain))[0].cpu().numpy()
+    q, scale, _ = sffn.rms_norm_fp8(to(x), to(gain))
+    assert scale.cpu().numpy()[0] == s and np.abs(y).max() == y[0, 0]
+    codes = lambda v: torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()  # noqa: E731
+    want = codes(y / s)
+    if size == 1.0:  # the inputs tell the two apart
+        assert (codes(y * (np.float32(1) / s)) != want).any()
+    assert np.array_equal(q.view(torch.uint8).cpu().numpy(), want)
