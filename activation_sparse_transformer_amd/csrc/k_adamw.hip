@@ -118,16 +118,16 @@ __device__ __forceinline__ void adamw_part(const AdamwTable& tab, const sffn_ada
     br = lane_reduce<64>(br, MaxNan()) / E4M3_MAX;
     bm = bm < SCALE_MIN ? SCALE_MIN : bm;
     br = br < SCALE_MIN ? SCALE_MIN : br;
-    const float im = 1.f / bm, ir = 1.f / br;
-    float a[4], b[4];
+    const Quotients over_m(bm), over_r(br);
+    over_m(m);
+    float b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = m[i] * im;
-      const float r = root[i] * ir;
-      b[i] = root[i] > 0.f && r < E4M3_TINY ? E4M3_TINY : r;
-    }
+    for (int i = 0; i < 4; ++i) b[i] = root[i];
+    over_r(b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = root[i] > 0.f && b[i] < E4M3_TINY ? E4M3_TINY : b[i];
     if (n > 0) {
-      store_codes4<NT>(static_cast<uint8_t*>(t.m) + e0, a, n);
+      store_codes4<NT>(static_cast<uint8_t*>(t.m) + e0, m, n);
       store_codes4<NT>(static_cast<uint8_t*>(t.v) + e0, b, n);
       if ((threadIdx.x & 63) == 0) {
         t.m_scale[blk] = bm;

@@ -133,8 +133,9 @@ typedef struct {
  * param is SFFN_F32 or SFFN_BF16, with an fp32 master only where it is SFFN_BF16; grad is
  * SFFN_F32 or SFFN_BF16.  state_bits 32 holds m and v in fp32.  state_bits 8 holds m and
  * r = sqrt(v) as e4m3 codes with one scale per 256 consecutive elements,
- * scale = max(absmax / 448, 2^-126); a positive r keeps at least the smallest positive code,
- * since it divides.  The step itself uses the unrounded m and r. */
+ * scale = max(absmax / 448, 2^-126), each code the e4m3 value nearest to the quotient by it; a
+ * positive r keeps at least the smallest positive code, since it divides.  The step itself uses
+ * the unrounded m and r. */
 sffn_status_t sffn_adamw_step(const sffn_adamw_tensor_t *tensors, int32_t n_tensors,
                               int32_t param_dtype, int32_t grad_dtype, int32_t state_bits,
                               const sffn_adamw_hyper_t *hyper, const float *grad_scale,

@@ -261,3 +261,32 @@ def test_refusals():
         with pytest.raises(sffn.SffnError) as ei:
             sffn.AdamW([p], **kw).step([p.clone()])
         assert ei.value.status == sffn.SFFN_ERR_INVALID_ARGUMENT
+
+
+def test_8bit_codes_are_of_the_quotient():
+    """The codes are e4m3(m / scale) and e4m3(r / scale) with the quotients in fp32, no reciprocal in
+    their place: first steps whose moments lie within a few roundings of the middle between two
+    codes.  From zero states both forms of the state compute the same m and v."""
+    torch, sffn = need_gpu()
+    n = 1 << 16
+    rng = np.random.default_rng(12)
+    v = np.array([(1 + m / 8) * 2.0 ** e for e in range(-6, 9) for m in range(8)][:-1])
+    mid = rng.choice((v[1:] + v[:-1]) / 2, n) * rng.choice([-1.0, 1.0], n)
+    top = np.repeat((1 + rng.random(n // 256)).astype(np.float32), 256)  # scales of many digits
+    g = (mid * (top.astype(np.float64) / 448)).astype(np.float32)
+    g = (g.view(np.int32) + rng.integers(-3, 4, n).astype(np.int32)).view(np.float32)
+    g[::256] = top[::256]
+    opts = []
+    for bits in (32, 8):
+        opts.append(sffn.AdamW([torch.zeros(n, device="cuda")], state_bits=bits, **HYPER))
+        opts[-1].step([torch.from_numpy(g).cuda()])
+    m = opts[0].state[0][0].cpu().numpy()
+    r = np.sqrt(opts[0].state[1][0].cpu().numpy())
+    codes = lambda a: torch.from_numpy(a).to(torch.float8_e4m3fn).view(torch.uint8).numpy()  # noqa: E731
+    for k, x in enumerate((m, r)):
+        s = opts[1].state[2 * k + 1][0].cpu().numpy()
+        assert np.array_equal(s, np.abs(x).reshape(-1, 256).max(1) / np.float32(448))
+        s = np.repeat(s, 256)
+        want = codes(x / s)
+        assert (codes(x * (np.float32(1) / s)) != want).any()  # the inputs tell the two apart
+        assert np.array_equal(opts[1].state[2 * k][0].view(torch.uint8).cpu().numpy(), want), k
