@@ -370,71 +370,103 @@ class AdamW:
     the root of the second as float8_e4m3fn with one float32 scale per 256 elements.  `state`
     continues from given tensors instead of zeros: [m, v] or [m, m_scale, r, r_scale], each a
     list like params; with it, state_bits goes by its length, and `step` is the number of steps
-    done.  The state tensors are in `.state`, in that order.  lr, betas, eps and weight_decay may be
-    changed between steps; a step recorded in a graph replays with those it was recorded with,
-    its number among them."""
+    done.
+
+    The tensors are in `.params`, `.master` and `.state`, in that order, as tuples: to replace
+    some, assign the whole (checked as here); a tensor whose storage was replaced (p.data = q)
+    is followed by the next step.  lr, betas, eps, weight_decay and steps may be changed between
+    steps; a step recorded in a graph replays with the values and the memory it was recorded
+    with, its number among them."""
 
     def __init__(self, params, master=None, state_bits=32, state=None, lr=1e-3,
                  betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=0):
-        f = _lib()
-        torch = f.torch
-        self.params = list(params)
-        if not self.params:
+        torch = _lib().torch
+        params = list(params)
+        if not params:
             raise ValueError("no parameters")
-        dt, dev = self.params[0].dtype, self.params[0].device
-        if dt not in (torch.float32, torch.bfloat16) or dev.type != "cuda":
-            raise ValueError("parameters must be float32 or bfloat16 device tensors")
-        for p in self.params:
-            _plain(p, "a parameter", dt, p.shape, dev)
-        used = [p.data_ptr() for p in self.params if p.numel()]
-        if len(set(used)) < len(used):
-            raise ValueError("a parameter is given twice")
-        self.master = None if master is None else list(master)
-        if self.master is not None and dt != torch.bfloat16:
-            raise ValueError("a master copy needs bfloat16 parameters")
+        dev = params[0].device
+        if dev.type != "cuda":
+            raise ValueError("parameters must be device tensors")
         if state is None:
             if state_bits not in (8, 32):
                 raise ValueError("state_bits must be 8 or 32")
-            zeros = lambda t, n: [torch.zeros(n(p), dtype=t, device=dev) for p in self.params]  # noqa: E731
+            zeros = lambda t, n: [torch.zeros(n(p), dtype=t, device=dev) for p in params]  # noqa: E731
             if state_bits == 32:
                 state = [zeros(torch.float32, lambda p: p.shape) for _ in range(2)]
             else:
                 state = [zeros(t, n) for _ in range(2) for t, n in (
                     (torch.float8_e4m3fn, lambda p: p.shape),
                     (torch.float32, lambda p: -(-p.numel() // ADAMW_BLOCK)))]
-        self.state = [list(k) for k in state]
-        if len(self.state) not in (2, 4):
+        self._bind(params, master, state)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.steps = int(step)
+
+    params = property(lambda self: self._params,
+                      lambda self, t: self._bind(t, self._master, self._state))
+    master = property(lambda self: self._master,
+                      lambda self, t: self._bind(self._params, t, self._state))
+    state = property(lambda self: self._state,
+                     lambda self, t: self._bind(self._params, self._master, t))
+    state_bits = property(lambda self: self._bits)
+    device = property(lambda self: self._device)
+    dtype = property(lambda self: self._params[0].dtype)
+
+    def _bind(self, params, master, state):
+        """Checks the tensors, then takes them and their addresses."""
+        f = _lib()
+        torch = f.torch
+        params = tuple(params)
+        if not params:
+            raise ValueError("no parameters")
+        dt, dev = params[0].dtype, params[0].device
+        if dt not in (torch.float32, torch.bfloat16) or dev.type != "cuda":
+            raise ValueError("parameters must be float32 or bfloat16 device tensors")
+        for p in params:
+            _plain(p, "a parameter", dt, p.shape, dev)
+        used = [p.data_ptr() for p in params if p.numel()]
+        if len(set(used)) < len(used):
+            raise ValueError("a parameter is given twice")
+        master = None if master is None else tuple(master)
+        if master is not None and dt != torch.bfloat16:
+            raise ValueError("a master copy needs bfloat16 parameters")
+        state = tuple(tuple(k) for k in state)
+        if len(state) not in (2, 4):
             raise ValueError("state must be [m, v] or [m, m_scale, r, r_scale]")
-        self.state_bits = 32 if len(self.state) == 2 else 8
-        for k in self.state + ([] if self.master is None else [self.master]):
-            if len(k) != len(self.params):
+        bits = 32 if len(state) == 2 else 8
+        for k in state + (() if master is None else (master,)):
+            if len(k) != len(params):
                 raise ValueError("master and state must have one tensor for each parameter")
-        for i, p in enumerate(self.params):
-            if self.master is not None:
-                _plain(self.master[i], "a master copy", torch.float32, p.shape, dev)
-            for j, k in enumerate(self.state):
-                if self.state_bits == 32:
+        for i, p in enumerate(params):
+            if master is not None:
+                _plain(master[i], "a master copy", torch.float32, p.shape, dev)
+            for j, k in enumerate(state):
+                if bits == 32:
                     _plain(k[i], "a state", torch.float32, p.shape, dev)
                 elif j % 2 == 0:
                     _plain(k[i], "a state", torch.float8_e4m3fn, p.shape, dev)
                 else:
                     _plain(k[i], "a state's scales", torch.float32,
                            (-(-p.numel() // ADAMW_BLOCK),), dev)
-        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
-        self.steps, self.device, self.dtype = int(step), dev, dt
-        self._t = (AdamwTensorC * len(self.params))()
-        for i, p in enumerate(self.params):
-            t = self._t[i]
+        table = (AdamwTensorC * len(params))()
+        for i, p in enumerate(params):
+            t = table[i]
             t.param, t.n = p.data_ptr(), p.numel()
-            t.master = _ptr(self.master[i]) if self.master is not None else None
-            if self.state_bits == 32:
-                t.m, t.v = (k[i].data_ptr() for k in self.state)
+            t.master = _ptr(master[i]) if master is not None else None
+            if bits == 32:
+                t.m, t.v = (k[i].data_ptr() for k in state)
             else:
-                t.m, t.m_scale, t.v, t.v_scale = (k[i].data_ptr() for k in self.state)
-        self._code = f.code[dt]
-        self._shapes = [p.shape for p in self.params]
-        # the same table as words, for the column of gradient pointers
-        self._words = np.frombuffer(self._t, dtype=np.uint64).reshape(len(self.params), -1)
+                t.m, t.m_scale, t.v, t.v_scale = (k[i].data_ptr() for k in state)
+        self._params, self._master, self._state = params, master, state
+        self._bits, self._device, self._code = bits, dev, f.code[dt]
+        self._shapes = [p.shape for p in params]
+        # all of them with the addresses in the table, and the memory behind those: kept, so that
+        # an address that is still the same is still the same memory
+        self._held = [t for k in (params, master or (), *state) for t in k]
+        self._ptrs = [t.data_ptr() for t in self._held]
+        self._memory = [t.detach() for t in self._held]
+        # the table, and as words, for the column of gradient pointers
+        self._t = table
+        self._words = np.frombuffer(table, dtype=np.uint64).reshape(len(params), -1)
 
     def step(self, grads, grad_scale=None, stream=None):
         """One step with grads (contiguous, shaped like params, all float32 or all bfloat16).
@@ -442,17 +474,18 @@ class AdamW:
         or unscaling factor, without a wait for the host)."""
         f = _lib()
         torch = f.torch
-        dev = self.device
+        T = torch.Tensor
+        dev = self._device
         if _elsewhere(f, dev, stream):
-            lists = [self.params, grads, self.master or [], *self.state]
-            with _on(dev, stream, grad_scale, *(t for k in lists for t in k)):
+            with _on(dev, stream, grad_scale, *self._held, *grads):
                 return self.step(grads, grad_scale)
-        if len(grads) != len(self.params):
+        if list(map(T.data_ptr, self._held)) != self._ptrs:  # a storage was replaced
+            self._bind(self._params, self._master, self._state)
+        if len(grads) != len(self._params):
             raise ValueError("one gradient for each parameter is needed")
         gt = grads[0].dtype
         if gt not in (torch.float32, torch.bfloat16):
             raise ValueError("gradients must be float32 or bfloat16")
-        T = torch.Tensor
         if list(map(_SHAPE, grads)) != self._shapes or set(map(_DTYPE, grads)) != {gt} \
                 or set(map(T.get_device, grads)) != {dev.index} \
                 or not all(map(T.is_contiguous, grads)):
@@ -464,9 +497,8 @@ class AdamW:
         self._words[:, _GRAD_WORD] = list(map(T.data_ptr, grads))
         b1, b2 = self.betas
         hp = AdamwHyperC(self.lr, b1, b2, self.eps, self.weight_decay, self.steps + 1)
-        st = f.sffn_adamw_step(self._t, len(self.params), self._code, f.code[gt],
-                               self.state_bits, ctypes.byref(hp), _ptr(grad_scale),
-                               f.stream(dev.index))
+        st = f.sffn_adamw_step(self._t, len(self._params), self._code, f.code[gt], self._bits,
+                               ctypes.byref(hp), _ptr(grad_scale), f.stream(dev.index))
         if st:
             _fail(st, "sffn_adamw_step")
         self.steps += 1

@@ -290,3 +290,43 @@ def test_8bit_codes_are_of_the_quotient():
         want = codes(x / s)
         assert (codes(x * (np.float32(1) / s)) != want).any()  # the inputs tell the two apart
         assert np.array_equal(opts[1].state[2 * k][0].view(torch.uint8).cpu().numpy(), want), k
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replaced_tensors(bits):
+    """A step works on the tensors as they stand: on a storage that replaced another's, and on
+    parameters, masters and states that were assigned; nothing can be replaced past the checks."""
+    torch, sffn = need_gpu()
+    sizes = [300, 5000]
+    params, grads, w = _make(torch, sizes, "bf16", "f32", True, 7)
+    opt = sffn.AdamW(params, master=w, state_bits=bits, **HYPER)
+    _step_and_check(torch, opt, grads, None, HYPER)
+    # new storages behind the same tensors; the old memory is left alone
+    old = [t.detach() for t in (params[1], w[0], opt.state[0][1])]
+    before = [t.clone() for t in old]
+    for t in (params[1], w[0], opt.state[0][1]):
+        t.data = t.clone()
+    _step_and_check(torch, opt, grads, None, HYPER)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(old, before))
+    # assigned lists
+    opt.state = [[t.clone() for t in k] for k in opt.state]
+    opt.master = [t.clone() for t in opt.master]
+    opt.params = [t.clone() for t in opt.params]
+    kept = [t.clone() for t in params + w]
+    _step_and_check(torch, opt, grads, None, HYPER)
+    assert all(torch.equal(a, b) for a, b in zip(params + w, kept))
+    # a single entry cannot be replaced, and what does not fit is refused and changes nothing
+    with pytest.raises(TypeError):
+        opt.state[0][0] = opt.state[0][0].clone()
+    for name, value in (("state", [[t[:5] for t in k] for k in opt.state]), ("state", opt.state[:1]),
+                        ("master", [t.double() for t in opt.master]), ("params", opt.params[:1]), ("params", [])):
+        with pytest.raises(ValueError):
+            setattr(opt, name, value)
+    for name in ("state_bits", "device", "dtype"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, getattr(opt, name))
+    _step_and_check(torch, opt, grads, None, HYPER)
+    p = opt.params[0]
+    p.data = p.float()
+    with pytest.raises(ValueError):
+        opt.step(grads)
