@@ -364,7 +364,8 @@ class Mx4Linear:
 class AdamW:
     """AdamW over a list of tensors, updated in place by one launch (per 48 tensors).
 
-    params: contiguous device tensors, all float32 or all bfloat16.  master: their float32
+    params: contiguous device tensors, all float32 or all bfloat16; none of the tensors that are
+    updated may overlap another.  master: their float32
     copies (for bfloat16 params), the values the step is taken on; params then receive the
     rounded result.  state_bits 32 keeps both moments in float32; 8 keeps the first moment and
     the root of the second as float8_e4m3fn with one float32 scale per 256 elements.  `state`
@@ -423,9 +424,6 @@ class AdamW:
             raise ValueError("parameters must be float32 or bfloat16 device tensors")
         for p in params:
             _plain(p, "a parameter", dt, p.shape, dev)
-        used = [p.data_ptr() for p in params if p.numel()]
-        if len(set(used)) < len(used):
-            raise ValueError("a parameter is given twice")
         master = None if master is None else tuple(master)
         if master is not None and dt != torch.bfloat16:
             raise ValueError("a master copy needs bfloat16 parameters")
@@ -447,6 +445,11 @@ class AdamW:
                 else:
                     _plain(k[i], "a state's scales", torch.float32,
                            (-(-p.numel() // ADAMW_BLOCK),), dev)
+        held = [t for k in (params, master or (), *state) for t in k]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in held if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):  # all of them are written
+            raise ValueError("two of the tensors (parameters, master copies, states) overlap")
         table = (AdamwTensorC * len(params))()
         for i, p in enumerate(params):
             t = table[i]
@@ -461,9 +464,8 @@ class AdamW:
         self._shapes = [p.shape for p in params]
         # all of them with the addresses in the table, and the memory behind those: kept, so that
         # an address that is still the same is still the same memory
-        self._held = [t for k in (params, master or (), *state) for t in k]
-        self._ptrs = [t.data_ptr() for t in self._held]
-        self._memory = [t.detach() for t in self._held]
+        self._held, self._ptrs = held, [t.data_ptr() for t in held]
+        self._memory = [t.detach() for t in held]
         # the table, and as words, for the column of gradient pointers
         self._t = table
         self._words = np.frombuffer(table, dtype=np.uint64).reshape(len(params), -1)

@@ -330,3 +330,31 @@ def test_replaced_tensors(bits):
     p.data = p.float()
     with pytest.raises(ValueError):
         opt.step(grads)
+
+
+def test_overlapping_tensors_are_refused():
+    """Every tensor that a step writes has memory of its own; neighbours in one buffer are fine."""
+    torch, sffn = need_gpu()
+    flat = torch.zeros(6000, device="cuda")
+    p, q, z = flat[:300], flat[300:600], [flat[1000 + 300 * i:1300 + 300 * i] for i in range(8)]
+    low = torch.zeros(900, device="cuda").bfloat16()
+    ok = sffn.AdamW([p, q], state=[z[:2], z[2:4]])
+    bad = [
+        lambda: sffn.AdamW([p, p]),
+        lambda: sffn.AdamW([p, flat[299:599]]),
+        lambda: sffn.AdamW([p], state=[[z[0]], [z[0]]]),
+        lambda: sffn.AdamW([p, q], state=[[z[0], z[1]], [z[2], z[0]]]),
+        lambda: sffn.AdamW([p], state=[[p], [z[0]]]),
+        lambda: sffn.AdamW([p], state=[[z[0]], [flat[200:500]]]),
+        lambda: sffn.AdamW([low[:300], low[300:600]], master=[z[0], z[0]]),
+        lambda: sffn.AdamW([low[:300]], master=[z[0]], state=[[z[1]], [z[0]]]),
+        lambda: sffn.AdamW([low[:300]], master=[low.view(torch.float32)[:300]]),
+        lambda: setattr(ok, "state", [z[:2], z[1:3]]),
+        lambda: setattr(ok, "params", [p, p]),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    e = flat[:0]
+    sffn.AdamW([e, p, e], state=[[e, z[0], e], [e, z[1], e]]).step([e, q, e])
+    ok.step([torch.ones_like(p), torch.ones_like(q)])
