@@ -287,7 +287,8 @@ class Mx4Linear:
     codes and scales are as mx4_quantize gives them (MXFP4: e2m1 values, one power of two per 32
     columns); in_features is K where it is not 32 * scales.shape[1].  They are laid out once for
     the kernel, here (a call on another stream has to wait for that), and not kept.  bias [N]
-    float32 is borrowed (kept referenced)."""
+    float32 is borrowed (kept referenced); it and relu may be assigned, and a bias whose storage
+    was replaced (bias.data = b) is followed by the next call."""
 
     def __init__(self, codes, scales, bias=None, relu=False, in_features=None, stream=None):
         f = _lib()
@@ -313,9 +314,26 @@ class Mx4Linear:
                                  f.stream(dev.index))
         if st:
             _fail(st, "sffn_mx4_tile")
-        self.in_features, self.out_features = K, N
-        self.bias, self.relu, self.tiled, self.device = bias, bool(relu), tiled, dev
+        self._n, self._k, self._bytes, self._device = N, K, n.value, dev
+        self.relu = bool(relu)
+        self._take(tiled, bias)
+
+    in_features = property(lambda self: self._k)
+    out_features = property(lambda self: self._n)
+    device = property(lambda self: self._device)
+    tiled = property(lambda self: self._tiled)
+    bias = property(lambda self: self._bias, lambda self, b: self._take(self._tiled, b))
+
+    def _take(self, tiled, bias):
+        """Checks the tensors, then takes them and their addresses.  The memory behind those is kept,
+        so that an address that is still the same is still the same memory."""
+        torch = _lib().torch
+        _plain(tiled, "tiled", torch.uint8, (self._bytes,), self._device)
+        if bias is not None:
+            _plain(bias, "bias", torch.float32, (self._n,), self._device)
+        self._tiled, self._bias = tiled, bias
         self._tiled_ptr, self._bias_ptr = tiled.data_ptr(), _ptr(bias)
+        self._memory = tiled.detach(), None if bias is None else bias.detach()
 
     @classmethod
     def from_dense(cls, W, bias=None, relu=False, stream=None):
@@ -329,10 +347,13 @@ class Mx4Linear:
         y; by default float32 for float32 x, otherwise bfloat16."""
         f = _lib()
         torch = f.torch
-        N, K, dev = self.out_features, self.in_features, self.device
+        N, K, dev, bias = self._n, self._k, self._device, self._bias
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream, x, x_scale, y, self.tiled, self.bias):
+            with _on(dev, stream, x, x_scale, y, self._tiled, bias):
                 return self(x, x_scale, dtype, y)
+        if self._tiled.data_ptr() != self._tiled_ptr \
+                or (bias is not None and bias.data_ptr() != self._bias_ptr):
+            self._take(self._tiled, bias)  # a storage was replaced
         shape = x.shape
         xc = f.code.get(x.dtype)
         if len(shape) != 2 or xc is None:

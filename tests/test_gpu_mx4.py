@@ -275,3 +275,39 @@ def test_refusals():
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def test_replaced_tensors():
+    """A call works on the bias and the weights as they stand, whether assigned or with another
+    storage behind them; what does not fit is refused and changes nothing."""
+    torch, sffn = need_gpu()
+    rng = np.random.default_rng(6)
+    codes, scales = _weights(rng, 40, 96)
+    to = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    bias = torch.zeros(40, device="cuda")
+    lin = sffn.Mx4Linear(to(codes), to(scales), bias=bias)
+    x = to(rng.standard_normal((3, 96)).astype(np.float32))
+    y0 = lin(x)
+    b = to(rng.standard_normal(40).astype(np.float32))
+    bias.data = b.clone()
+    assert torch.equal(lin(x), y0 + b)
+    lin.bias = 2 * b
+    assert torch.equal(lin(x), y0 + 2 * b) and torch.equal(lin.bias, 2 * b)
+    for bad in (b[:39], b.double(), b.cpu(), torch.zeros(80, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            lin.bias = bad
+    assert torch.equal(lin(x), y0 + 2 * b)
+    lin.bias = None
+    assert torch.equal(lin(x), y0)
+    lin.relu = True
+    assert torch.equal(lin(x), y0.clamp_min(0))
+    lin.relu = False
+    other = sffn.Mx4Linear(to(codes ^ 0x88), to(scales))  # every sign turned
+    lin.tiled.data = other.tiled.clone()
+    assert torch.equal(lin(x), other(x)) and not torch.equal(other(x), y0)
+    lin.tiled.data = other.tiled[:-1].clone()
+    with pytest.raises(ValueError):
+        lin(x)
+    for name in ("tiled", "in_features", "out_features", "device"):
+        with pytest.raises(AttributeError):
+            setattr(lin, name, getattr(lin, name))
