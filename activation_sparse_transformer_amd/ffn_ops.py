@@ -4,8 +4,11 @@ RMS norm with the residual's sum and its gradient, products with 4-bit weights, 
 Argument marshalling only, as in ``sparse_ffn``: every step runs in the library's HIP kernels;
 PyTorch supplies device memory and the stream.  With ``stream=None`` a call runs on PyTorch's
 current stream of the tensors' device; a given ``stream`` is used for the kernels and for what
-the call allocates.  Tensors made on another stream have to be ready on it (the caller's events);
-their memory is not given away before the call's work is done.
+the call allocates.  Tensors made on another stream have to be ready on it (the caller's events).
+Memory is not given away before the call's work is done: that of every tensor of a call with a
+given stream, and on whatever stream a call runs that of what an ``Mx4Linear`` or ``AdamW`` holds.
+As with PyTorch's own operations, the other tensors of a call on the current stream are the
+caller's to keep (``record_stream``) if they were allocated on a different one.
 """
 from __future__ import annotations
 
@@ -122,6 +125,23 @@ def _on(device, stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+
+
+class _Held:
+    """Tensors that an object keeps from call to call: their memory stays theirs until every stream
+    that a call ran on is past it, also after the object is gone."""
+
+    def __init__(self, tensors):
+        self._tensors = [t.detach() for t in tensors]  # (not a storage that takes their place)
+        self._streams = set()
+
+    def used_on(self, f, device, stream):
+        """Called with each call's stream handle, which is current."""
+        if stream not in self._streams:
+            current = f.torch.cuda.current_stream(device)
+            for t in self._tensors:
+                t.record_stream(current)
+            self._streams.add(stream)
 
 
 def _matrix(t, name, dtype, shape, device):
@@ -325,7 +345,7 @@ class Mx4Linear:
     bias = property(lambda self: self._bias, lambda self, b: self._take(self._tiled, b))
 
     def _take(self, tiled, bias):
-        """Checks the tensors, then takes them and their addresses.  The memory behind those is kept,
+        """Checks the tensors, then takes them and their addresses.  The memory behind those is held,
         so that an address that is still the same is still the same memory."""
         torch = _lib().torch
         _plain(tiled, "tiled", torch.uint8, (self._bytes,), self._device)
@@ -333,7 +353,7 @@ class Mx4Linear:
             _plain(bias, "bias", torch.float32, (self._n,), self._device)
         self._tiled, self._bias = tiled, bias
         self._tiled_ptr, self._bias_ptr = tiled.data_ptr(), _ptr(bias)
-        self._memory = tiled.detach(), None if bias is None else bias.detach()
+        self._held = _Held([tiled] if bias is None else [tiled, bias])
 
     @classmethod
     def from_dense(cls, W, bias=None, relu=False, stream=None):
@@ -349,7 +369,7 @@ class Mx4Linear:
         torch = f.torch
         N, K, dev, bias = self._n, self._k, self._device, self._bias
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream, x, x_scale, y, self._tiled, bias):
+            with _on(dev, stream, x, x_scale, y):
                 return self(x, x_scale, dtype, y)
         if self._tiled.data_ptr() != self._tiled_ptr \
                 or (bias is not None and bias.data_ptr() != self._bias_ptr):
@@ -374,9 +394,10 @@ class Mx4Linear:
             if dt not in (torch.float32, torch.bfloat16) or dtype not in (None, dt):
                 raise ValueError("y must be float32 or bfloat16, and of `dtype`")
             _plain(y, "y", dt, (T, N), dev)
+        s = f.stream(dev.index)
+        self._held.used_on(f, dev, s)
         st = f.sffn_mx4_linear(self._tiled_ptr, N, K, xc, x.data_ptr(), xs, _ptr(x_scale), T,
-                               self._bias_ptr, self.relu, f.code[dt], y.data_ptr(),
-                               f.stream(dev.index))
+                               self._bias_ptr, self.relu, f.code[dt], y.data_ptr(), s)
         if st:
             _fail(st, "sffn_mx4_linear")
         return y
@@ -483,10 +504,10 @@ class AdamW:
         self._params, self._master, self._state = params, master, state
         self._bits, self._device, self._code = bits, dev, f.code[dt]
         self._shapes = [p.shape for p in params]
-        # all of them with the addresses in the table, and the memory behind those: kept, so that
+        # all of them with the addresses in the table, and the memory behind those: held, so that
         # an address that is still the same is still the same memory
-        self._held, self._ptrs = held, [t.data_ptr() for t in held]
-        self._memory = [t.detach() for t in held]
+        self._tensors, self._ptrs = held, [t.data_ptr() for t in held]
+        self._held = _Held(held)
         # the table, and as words, for the column of gradient pointers
         self._t = table
         self._words = np.frombuffer(table, dtype=np.uint64).reshape(len(params), -1)
@@ -500,9 +521,9 @@ class AdamW:
         T = torch.Tensor
         dev = self._device
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream, grad_scale, *self._held, *grads):
+            with _on(dev, stream, grad_scale, *grads):
                 return self.step(grads, grad_scale)
-        if list(map(T.data_ptr, self._held)) != self._ptrs:  # a storage was replaced
+        if list(map(T.data_ptr, self._tensors)) != self._ptrs:  # a storage was replaced
             self._bind(self._params, self._master, self._state)
         if len(grads) != len(self._params):
             raise ValueError("one gradient for each parameter is needed")
@@ -520,8 +541,10 @@ class AdamW:
         self._words[:, _GRAD_WORD] = list(map(T.data_ptr, grads))
         b1, b2 = self.betas
         hp = AdamwHyperC(self.lr, b1, b2, self.eps, self.weight_decay, self.steps + 1)
+        s = f.stream(dev.index)
+        self._held.used_on(f, dev, s)
         st = f.sffn_adamw_step(self._t, len(self._params), self._code, f.code[gt], self._bits,
-                               ctypes.byref(hp), _ptr(grad_scale), f.stream(dev.index))
+                               ctypes.byref(hp), _ptr(grad_scale), s)
         if st:
             _fail(st, "sffn_adamw_step")
         self.steps += 1

@@ -99,3 +99,64 @@ def test_serving_in_a_graph():
         ref.step([g])
         assert torch.equal(p, before[0]) and torch.equal(opt.state[1][0], before[2])
         torch.cuda.synchronize()
+
+
+def _busy(torch):
+    """Some tenths of a second of work on the current stream, and an event behind it."""
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    b = torch.empty_like(a)
+    for _ in range(300):
+        torch.mm(a, a, out=b)
+    return b
+
+
+@pytest.mark.parametrize("with_stream", [False, True])
+@pytest.mark.parametrize("what", ["weights", "bias", "8-bit states", "replaced states"])
+def test_held_memory_outlives_its_owner(what, with_stream):
+    """What a layer or an optimizer holds is not given to another tensor of its stream while a
+    call on a different stream has yet to run, also with stream=None: the owner goes (or takes
+    other tensors) while the call waits behind other work."""
+    torch, sffn = need_gpu()
+    n = 3 << 20
+    x = torch.randn((2, 1024), device="cuda")
+    W = torch.randn((4096, 1024), device="cuda")
+    side, home = torch.cuda.Stream(), torch.cuda.Stream()
+    busy = _busy(torch)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(home):  # the allocations' stream
+        if what == "weights":
+            own = sffn.Mx4Linear.from_dense(W)
+            hold = [own.tiled]
+        elif what == "bias":
+            own = sffn.Mx4Linear.from_dense(W.repeat(1024, 1)[:n // 4, :32], bias=torch.zeros(n // 4, device="cuda"))
+            x = x[:, :32].contiguous()
+            hold = [own.bias]
+        else:
+            own = sffn.AdamW([torch.ones(n, device="cuda")], state_bits=8)
+            g = torch.ones(n, device="cuda")
+            hold = [own.state[0][0], own.state[2][0]]
+    torch.cuda.synchronize()
+    ptrs = [t.data_ptr() for t in hold]
+    sizes = [t.numel() * t.element_size() for t in hold]
+    with torch.cuda.stream(side):
+        busy = _busy(torch)
+        done = torch.cuda.Event()
+        done.record()
+    call = (lambda **k: own.step([g], **k)) if "states" in what else (lambda **k: own(x, **k))
+    if with_stream:
+        call(stream=side)
+    else:
+        with torch.cuda.stream(side):
+            call()
+    with torch.cuda.stream(home):
+        if what == "replaced states":
+            own.state = [[t.clone() for t in k] for k in own.state]
+            del hold
+        else:
+            del own, hold, call
+        new = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(3)]
+    assert not done.query()  # the call has not run yet
+    assert not set(ptrs) & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    assert float(busy[0, 0]) == 8192.0
