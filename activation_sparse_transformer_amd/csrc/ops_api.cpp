@@ -45,6 +45,41 @@ sffn_status_t check_matrix(const void* p, int64_t stride, int64_t rows, int32_t 
   return SFFN_OK;
 }
 
+// Rows of bytes in device memory: `rows` of `width`, `pitch` apart (from one block: one row).
+struct Rows {
+  uintptr_t at;
+  uint64_t rows, pitch, width;
+};
+Rows block(const void* p, uint64_t bytes) { return Rows{reinterpret_cast<uintptr_t>(p), 1, 0, bytes}; }
+// A [rows, d] matrix; rows that follow one another without a gap are one block.
+Rows matrix(const void* p, int64_t stride, int64_t rows, int64_t d, size_t size) {
+  if (rows <= 1 || stride == d) return block(p, (uint64_t)rows * d * size);
+  return Rows{reinterpret_cast<uintptr_t>(p), (uint64_t)rows, stride * size, d * size};
+}
+// Whether a block of memory meets any of the rows (neither is there if its address is NULL).
+bool overlap(const Rows& out, const Rows& r) {
+  if (!out.at || !r.at || !out.width || !r.width) return false;
+  const uintptr_t end = out.at + out.width;
+  if (end <= r.at) return false;
+  uint64_t i = 0;  // the first row that ends past the block's start
+  if (out.at >= r.at + r.width) {
+    if (r.rows == 1) return false;
+    i = (out.at - r.at - r.width) / r.pitch + 1;
+  }
+  return i < r.rows && r.at + i * r.pitch < end;
+}
+// Refuses outputs (blocks) that overlap an input or each other.
+template <size_t N, size_t M>
+sffn_status_t check_overlap(const Rows (&out)[N], const Rows (&in)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (const Rows& r : in)
+      if (overlap(out[i], r)) return invalid("an output overlaps an input");
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return invalid("two outputs overlap");
+  }
+  return SFFN_OK;
+}
+
 sffn_status_t norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_stride,
                    const void* residual, int64_t residual_stride, const void* gain, float eps,
                    int64_t rows, int32_t d, void* y, float* stat, void* h, bool fp8,
@@ -63,6 +98,24 @@ sffn_status_t norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_s
   if (misaligned(gain, size_of(gain_dtype)) || misaligned(y, fp8 ? 1 : size_of(dtype)) ||
       misaligned(h, size_of(dtype)) || misaligned(stat, 4))
     return invalid("a pointer is not aligned to its element");
+  const size_t size = size_of(dtype);
+  const Rows xr = matrix(x, x_stride, rows, d, size),
+             rr = matrix(residual, residual_stride, rows, d, size),
+             yr = block(y, (uint64_t)rows * d * (fp8 ? 1 : size)),
+             hr = block(h, (uint64_t)rows * d * size),
+             sr = block(stat, (uint64_t)rows * 4);
+  // a row is in registers before any of it is written, so that h, and y of the same type, may take
+  // the place of x or the residual
+  const Rows none = block(nullptr, 0), gr = block(gain, (uint64_t)d * size_of(gain_dtype));
+  const auto in_place = [](const Rows& o, const Rows& i) {
+    return o.at == i.at && o.width == i.width && i.rows == 1;
+  };
+  for (const Rows* i : {&xr, &rr}) {
+    OPS_TRY(check_overlap({hr}, {in_place(hr, *i) ? none : *i}));
+    OPS_TRY(check_overlap({yr}, {!fp8 && in_place(yr, *i) ? none : *i}));
+  }
+  OPS_TRY(check_overlap({yr, hr, sr}, {gr}));
+  OPS_TRY(check_overlap({sr}, {xr, rr}));
   const NormArgs a{x, x_stride, residual, residual ? residual_stride : 0, gain, eps, rows, d, y, stat, h};
   auto f = [&] {
     return launch_rms_norm(dtype == SFFN_BF16, gain_dtype == SFFN_F32, fp8, a,
@@ -133,6 +186,16 @@ sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const vo
     if (dgain && groups > 0 && (!workspace || misaligned(workspace, 16) ||
                                 workspace_bytes < (size_t)groups * d * sizeof(float)))
       return invalid("workspace is NULL, misaligned or too small");
+    const size_t size = size_of(dtype);
+    const Rows dxr = block(dx, (uint64_t)rows * d * size), dgr = block(dgain, (uint64_t)d * 4),
+               wr = block(dgain && groups > 0 ? workspace : nullptr, (uint64_t)groups * d * 4),
+               dyr = matrix(dy, dy_stride, rows, d, size), hr = matrix(h, h_stride, rows, d, size),
+               gr = block(gain, (uint64_t)d * size_of(gain_dtype)),
+               sr = block(rstd, (uint64_t)rows * 4),
+               rr = matrix(dres, dres_stride, rows, d, size);
+    OPS_TRY(check_overlap({dxr, dgr, wr}, {dyr, hr, gr, sr}));
+    OPS_TRY(check_overlap({dgr, wr}, {rr}));
+    if (dx != dres || rr.rows > 1) OPS_TRY(check_overlap({dxr}, {rr}));
     const NormGradArgs a{dy, dy_stride, h, h_stride, gain, rstd, dres, dres ? dres_stride : 0,
                          rows, d, dx, dgain, dgain && groups > 0 ? part : nullptr};
     auto f = [&] { return launch_rms_norm_grad(dtype == SFFN_BF16, gain_dtype == SFFN_F32, a, s); };
@@ -150,6 +213,9 @@ sffn_status_t sffn_mx4_quantize(int32_t dtype, const void* W, int64_t w_stride, 
   if (N == 0) return SFFN_OK;
   OPS_TRY(check_matrix(W, w_stride, N, K, dtype, "W is NULL", "w_stride is less than K"));
   if (!codes || !scales) return invalid("codes or scales is NULL");
+  const uint64_t groups = (uint64_t)N * ((K + 31) / 32);
+  OPS_TRY(check_overlap({block(codes, groups * 16), block(scales, groups)},
+                        {matrix(W, w_stride, N, K, size_of(dtype))}));
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto f = [&] { return launch_mx4_quantize(dtype == SFFN_BF16, W, w_stride, N, K, codes, scales, s); };
   return api_run("mx4_quantize", s, f);
@@ -168,6 +234,9 @@ sffn_status_t sffn_mx4_tile(const uint8_t* codes, const uint8_t* scales, int32_t
   if (N == 0) return SFFN_OK;
   if (!codes || !scales || !tiled) return invalid("codes, scales or tiled is NULL");
   if (misaligned(tiled, 16)) return invalid("tiled must be 16-byte aligned");
+  const uint64_t groups = (uint64_t)N * ((K + 31) / 32);
+  OPS_TRY(check_overlap({block(tiled, mx4_dims(N, K).bytes())},
+                        {block(codes, groups * 16), block(scales, groups)}));
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto f = [&] { return launch_mx4_tile(codes, scales, mx4_dims(N, K), tiled, s); };
   return api_run("mx4_tile", s, f);
@@ -191,6 +260,10 @@ sffn_status_t sffn_mx4_linear(const void* tiled, int32_t N, int32_t K, int32_t x
   if (misaligned(tiled, 16)) return invalid("tiled must be 16-byte aligned");
   if (misaligned(y, size_of(y_dtype)) || misaligned(x_scale, 4) || misaligned(bias, 4))
     return invalid("a pointer is not aligned to its element");
+  OPS_TRY(check_overlap({block(y, (uint64_t)T * N * size_of(y_dtype))},
+                        {block(tiled, mx4_dims(N, K).bytes()),
+                         matrix(x, x_stride, T, K, size_of(x_dtype)),
+                         block(x_scale, (uint64_t)T * 4), block(bias, (uint64_t)N * 4)}));
   const Mx4Args a{tiled, mx4_dims(N, K), x_dtype, x, x_stride, x_scale, T, bias, relu != 0,
                   y_dtype == SFFN_BF16, y};
   auto f = [&] { return launch_mx4_linear(a, static_cast<hipStream_t>(stream)); };
@@ -232,6 +305,11 @@ sffn_status_t sffn_adamw_step(const sffn_adamw_tensor_t* tensors, int32_t n_tens
         misaligned(t.v, sa) || misaligned(t.master, 4) || misaligned(t.m_scale, 4) ||
         misaligned(t.v_scale, 4))
       return invalid("a pointer is not aligned to its element");
+    const uint64_t n = (uint64_t)t.n, blocks = (n + SFFN_ADAMW_BLOCK - 1) / SFFN_ADAMW_BLOCK,
+                   scales = state_bits == 8 ? blocks * 4 : 0;
+    OPS_TRY(check_overlap({block(t.param, n * pa), block(t.master, n * 4), block(t.m, n * sa),
+                           block(t.v, n * sa), block(t.m_scale, scales), block(t.v_scale, scales)},
+                          {block(t.grad, n * ga)}));
   }
   // Complements and powers in double: in fp32, 1 - beta2 would lose the digits of a small
   // difference.

@@ -213,7 +213,8 @@ def rms_norm(x, gain, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream
     """h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * gain over the rows of
     x [rows, d] (float32 or bfloat16; rows may be strided).  gain [d] has x's type or float32.
     Returns (y, h, rstd): what rms_norm_backward takes; h is x without a residual.  y, h and
-    rstd may be given to be overwritten; h may be the (contiguous) residual or x itself."""
+    rstd may be given to be overwritten; y and h may each be the (contiguous) residual or x
+    itself, otherwise they may not overlap anything."""
     y, rstd, h = _norm(_lib().sffn_rms_norm, False, x, gain, residual, eps, y, rstd, h, stream)
     return y, h, rstd
 
@@ -230,7 +231,8 @@ def rms_norm_backward(dy, h, gain, rstd, dres=None, with_dgain=True, dx=None, dg
     """Gradient of rms_norm for dL/dy = dy, with the forward's h and rstd.  dres is the gradient
     that reaches h past the norm (of the residual stream).  Returns (dx, dgain): dx, in h's
     type, is the gradient of both x and the residual; dgain is float32, or None without
-    with_dgain.  dx may be given (also dres itself), and dgain."""
+    with_dgain.  dx and dgain may be given; dx may be dres itself, otherwise they may not overlap
+    anything (dgain's sums read dy and h while dx is written)."""
     f = _lib()
     torch = f.torch
     dev, dt = h.device, h.dtype

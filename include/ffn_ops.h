@@ -10,8 +10,9 @@
  *   - A row stride counts elements from one row to the next (>= the row's length); the elements
  *     of a row are contiguous.  Pointers need only their element's alignment.
  *   - Zero rows (or elements, or tensors) are valid and launch nothing.
- *   - No output may overlap an input, except where a call says that it updates in place, and
- *     rms_norm's h, which may be x or the residual itself (same address and stride).
+ *   - No output may overlap an input or another output (SFFN_ERR_INVALID_ARGUMENT), except where
+ *     a call says that it updates in place, and the norm's h, and its y in dtype, which may be x
+ *     or the residual itself (same address and stride).
  *   - Non-finite values follow the formulas: they reach the outputs that depend on them.
  *   - Results do not depend on timing: no call adds with atomics.
  *   - Kernel names for sffn_profile_read: rms_norm, rms_norm_fp8, rms_norm_grad,
@@ -52,8 +53,8 @@ sffn_status_t sffn_rms_norm(int32_t dtype, int32_t gain_dtype, const void *x, in
 
 /* The same norm with its output in 8 bits and one scale a row, the form sffn_mx4_linear takes:
  *   scale = max(max_i |y_i| / 448, 2^-126),  q = e4m3(y / scale)
- * (the quotient rounded to fp32, then to nearest-even).  q [rows, d] bytes, scale [rows] fp32.  A row of zeros gives zeros; a NaN or an infinity in a
- * row gives a scale that is not finite. */
+ * (the quotient rounded to fp32, then to nearest-even).  q [rows, d] bytes, scale [rows] fp32.
+ * A row of zeros gives zeros; a NaN or an infinity in a row gives a scale that is not finite. */
 sffn_status_t sffn_rms_norm_fp8(int32_t dtype, int32_t gain_dtype, const void *x,
                                 int64_t x_stride, const void *residual, int64_t residual_stride,
                                 const void *gain, float eps, int64_t rows, int32_t d, void *q,
@@ -135,7 +136,8 @@ typedef struct {
  * r = sqrt(v) as e4m3 codes with one scale per 256 consecutive elements,
  * scale = max(absmax / 448, 2^-126), each code the e4m3 value nearest to the quotient by it; a
  * positive r keeps at least the smallest positive code, since it divides.  The step itself uses
- * the unrounded m and r. */
+ * the unrounded m and r.  The arrays of a tensor are checked for overlap; different tensors are
+ * the caller's to keep apart. */
 sffn_status_t sffn_adamw_step(const sffn_adamw_tensor_t *tensors, int32_t n_tensors,
                               int32_t param_dtype, int32_t grad_dtype, int32_t state_bits,
                               const sffn_adamw_hyper_t *hyper, const float *grad_scale,

@@ -382,3 +382,39 @@ def test_fp8_codes_are_of_the_quotient(size):
     if size == 1.0:  # the inputs tell the two apart
         assert (codes(y * (np.float32(1) / s)) != want).any()
     assert np.array_equal(q.view(torch.uint8).cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ overlap
+
+@pytest.mark.parametrize("d", [100, 513, 2304, 5000])
+def test_norm_output_in_place_and_between_rows(d):
+    """y in place of x or the residual gives the same bits, and so does an output that lies in the
+    gap between strided rows; outputs over parts of inputs are refused."""
+    torch, sffn = need_gpu()
+    dt = torch.bfloat16
+    x, res = _rows(torch, 21, d, dt, 1), _rows(torch, 21, d, dt, 2)
+    gain = (1 + 0.1 * _rows(torch, 1, d, dt, 5)[0]).contiguous()
+    y0, h0, r0 = sffn.rms_norm(x, gain, residual=res)
+    a, b = x.clone(), res.clone()
+    y, h, r = sffn.rms_norm(a, gain, residual=b, y=a, h=b)
+    assert y is a and h is b and torch.equal(a, y0) and torch.equal(b, h0) and torch.equal(r, r0)
+    a, b = x.clone(), res.clone()
+    sffn.rms_norm(a, gain, residual=b, y=b, h=a)
+    assert torch.equal(b, y0) and torch.equal(a, h0)
+    wide = torch.zeros((2, 30 * d), dtype=dt, device="cuda")
+    wide[:, :d] = x[:2]
+    gap = wide[0, d + 1:3 * d + 1].view(2, d)
+    y, _, _ = sffn.rms_norm(wide[:, :d], gain, residual=res[:2].contiguous(), y=gap)
+    assert torch.equal(gap, y0[:2]) and torch.equal(wide[:, :d], x[:2])
+    flat = torch.zeros(4 * d + 2, dtype=dt, device="cuda")
+    two = flat[:2 * d].view(2, d)
+    for bad in (lambda: sffn.rms_norm(two, gain, y=flat[2:2 * d + 2].view(2, d)),
+                lambda: sffn.rms_norm(wide[:, :d], gain, y=wide[0, :2 * d].view(2, d)),
+                lambda: sffn.rms_norm(two, gain, residual=two.clone(), y=flat[2 * d:4 * d].view(2, d),
+                                      h=flat[2 * d:4 * d].view(2, d)),
+                lambda: sffn.rms_norm_backward(x, h0, gain, r0, dx=x),
+                lambda: sffn.rms_norm_backward(x, h0, gain, r0, dres=x, dx=x),
+                lambda: sffn.rms_norm_backward(x, h0, gain, r0, dx=h0)):
+        with pytest.raises(sffn.SffnError) as ei:
+            bad()
+        assert ei.value.status == sffn.SFFN_ERR_INVALID_ARGUMENT

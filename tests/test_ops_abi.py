@@ -160,3 +160,80 @@ def test_binding_needs_device_tensors(ops):
                  lambda: ops.AdamW([x])):
         with pytest.raises(ValueError):
             call()
+
+
+def _message():
+    from activation_sparse_transformer_amd import sparse_ffn
+    return sparse_ffn.last_error()
+
+
+B = 1 << 28  # distance of the stand-in arrays below: more than any of them is long
+
+
+@pytest.mark.parametrize("kw", [
+    {"h": 1 * B + 128}, {"h": 2 * B - 2}, {"h": 4 * B}, {"h": 3 * B}, {"h": 5 * B}, {"y": 1 * B + 2}, {"y": 1 * B + 64 * 2 * 9 + 126},
+    {"y": 2 * B + 2}, {"y": 3 * B - 2}, {"y": 5 * B}, {"stat": 1 * B}, {"stat": 2 * B + 4}, {"stat": 3 * B + 124}, {"stat": 4 * B},
+    # in place only with the same stride, and a row's own type
+    {"x_stride": 80, "h": 1 * B}, {"x_stride": 80, "y": 1 * B}, {"residual_stride": 65, "h": 2 * B},
+    {"x_stride": 80, "y": 1 * B + 80 * 2 * 9},
+])
+def test_norm_overlap(ops, kw):
+    """Outputs over inputs or one another, by a whole array, by its edge, or in a strided row."""
+    a = dict(NORM, rows=10, x=1 * B, residual=2 * B, gain=3 * B, y=4 * B, h=None, stat=5 * B)
+    a.update(kw)
+    for fn in ("sffn_rms_norm", "sffn_rms_norm_fp8"):
+        assert getattr(ops._lib(), fn)(*a.values(), None) == INVALID and "overlap" in _message(), fn
+
+
+def test_norm_fp8_is_not_in_place(ops):
+    a = dict(NORM, rows=10, x=1 * B, residual=2 * B, gain=3 * B, y=1 * B, h=None, stat=5 * B)
+    assert ops._lib().sffn_rms_norm_fp8(*a.values(), None) == INVALID and "overlap" in _message()
+
+
+@pytest.mark.parametrize("rows", [40, 5000])  # dgain summed beside the rows, and in a second launch
+@pytest.mark.parametrize("kw", [
+    {"dx": "dy"}, {"dx": "h"}, {"dx": "dy", "dres": "dy"}, {"dx": "h", "dgain": None}, {"dx": "gain"}, {"dx": "rstd"},
+    {"dres_stride": 66, "dx": "dres"}, {"dgain": "gain"}, {"dgain": "dy"}, {"dgain": "dres"}, {"dgain": "dx"},
+    {"dgain": "rstd"},
+])
+def test_norm_backward_overlap(ops, rows, kw):
+    at = {k: (i + 1) * B for i, k in enumerate(("dy", "h", "gain", "rstd", "dres", "dx", "dgain", "ws"))}
+    a = dict(GRAD, rows=rows, **at)
+    a.update({k: at.get(v, v) for k, v in kw.items()})
+    assert ops._lib().sffn_rms_norm_backward(*a.values(), None) == INVALID and "overlap" in _message()
+    edge = dict(GRAD, rows=rows, **at)
+    edge["dx"] = at["dy"] + (rows - 1) * 128 + 126  # the last element
+    assert ops._lib().sffn_rms_norm_backward(*edge.values(), None) == INVALID and "overlap" in _message()
+
+
+def test_norm_backward_workspace_overlap(ops):
+    at = {k: (i + 1) * B for i, k in enumerate(("dy", "h", "gain", "rstd", "dres", "dx", "dgain", "ws"))}
+    for k in ("dy", "h", "gain", "rstd", "dres", "dx", "dgain"):
+        a = dict(GRAD, **dict(at, ws=at[k]))
+        assert ops._lib().sffn_rms_norm_backward(*a.values(), None) == INVALID and "overlap" in _message(), k
+
+
+def test_mx4_overlap(ops):
+    f = ops._lib()
+    a = dict(tiled=1 * B, N=48, K=64, x_dtype=BF16, x=2 * B, x_stride=64, x_scale=3 * B, T=3, bias=4 * B, relu=1,
+             y_dtype=F32, y=5 * B)
+    for y in (1 * B, 1 * B + 1088 * 3 - 4, 2 * B, 2 * B + 2 * 128 + 124, 2 * B - 4, 3 * B + 8, 4 * B, 4 * B + 47 * 4):
+        assert f.sffn_mx4_linear(*dict(a, y=y).values(), None) == INVALID and "overlap" in _message(), y
+    far = dict(a, x_stride=1000, y=2 * B + 2000 * 2)  # over the last row
+    assert f.sffn_mx4_linear(*far.values(), None) == INVALID and "overlap" in _message()
+    for codes, scales in ((1 * B, 2 * B), (1 * B + 16 * 32 * 4 - 1, 2 * B), (2 * B, 1 * B), (2 * B, 2 * B + 16), (2 * B, 2 * B)):
+        assert f.sffn_mx4_quantize(F32, 1 * B, 32, 16, 32, codes, scales, None) == INVALID and "overlap" in _message()
+    for tiled in (1 * B, 2 * B, 2 * B - 16, 1 * B + 16 * 15):
+        assert f.sffn_mx4_tile(1 * B, 2 * B, 16, 32, tiled, None) == INVALID and "overlap" in _message()
+
+
+@pytest.mark.parametrize("kw,bits", [
+    ({"grad": "param"}, 32), ({"grad": "m"}, 32), ({"v": "m"}, 32), ({"m": "param"}, 32), ({"master": "param"}, 32),
+    ({"master": "v"}, 32), ({"m_scale": "v_scale"}, 8), ({"m_scale": "m"}, 8), ({"v": "m"}, 8), ({"grad": "v_scale"}, 8),
+])
+def test_adamw_overlap(ops, kw, bits):
+    at = {k: (i + 1) * B for i, k in enumerate(("param", "grad", "master", "m", "v", "m_scale", "v_scale"))}
+    t = ops.AdamwTensorC(n=300, **dict(at, **{k: at[v] for k, v in kw.items()}))
+    h = ops.AdamwHyperC(**HYPER)
+    assert ops._lib().sffn_adamw_step(ctypes.byref(t), 1, BF16, F32, bits, ctypes.byref(h), None, None) == INVALID
+    assert "overlap" in _message()
