@@ -12,6 +12,9 @@
 //
 // Bound by reading the weights at few tokens: 65536 x 8192 at 4 tokens 50.2 us (5.7 TB/s); at 64
 // tokens and many rows by expansion and products (65536 x 2048 bf16 31 us, e4m3 28).
+#include <utility>
+
+#include "mx4_shape.hpp"
 #include "ops_common.hpp"
 
 namespace sffn {
@@ -188,8 +191,6 @@ __device__ __forceinline__ void mx4_store(const Mx4Args& a, f32x4 s, int tok, in
   }
 }
 
-constexpr int MX4_WAVES = 8;
-
 // Orders a wave's accesses to its own piece of LDS: the hardware carries them out in order, only
 // the compiler has to keep it.
 __device__ __forceinline__ void wave_fence() {
@@ -235,20 +236,13 @@ struct Mx4Weights {
   }
 };
 
-// Whether two workgroups fit a CU: 128 registers and half of the LDS do without spilling.
-template <int XT, int TT, int RB>
-constexpr bool mx4_pairs() {
-  return TT == 1 || (XT == SFFN_E4M3 && RB * TT <= (TT == 2 ? 6 : 8)) ||
-         (XT == SFFN_BF16 && RB * TT <= 4 && TT == 2);
-}
-
 // KS of a workgroup's waves split k, the others take further rows.  Rows past the end are read as
 // the last one and not stored; what a column without a token holds is not stored either (a
 // product's columns do not mix).  More than 16 tokens are turned in LDS; up to 16 each lane loads
 // its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048).
 // Many waves hide the loads: a second block of columns in flight in a wave gained nothing.
 template <int XT, int TT, int RB, int KS>
-__global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs<XT, TT, RB>() ? 4 : 2)) void
+__global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs(XT, TT, RB) ? 4 : 2)) void
 mx4_linear_kernel(Mx4Args a) {
   typedef TokTile<XT> Tile;
   typedef typename Tile::E E;
@@ -340,86 +334,31 @@ mx4_linear_kernel(Mx4Args a) {
 }
 
 template <int XT, int TT, int RB, int KS>
-hipError_t launch_ks(const Mx4Args& a, hipStream_t s) {
+hipError_t launch_form(const Mx4Args& a, hipStream_t s) {
   constexpr int ROWS = RB * MX4_WAVES / KS;
-  const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
+  const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)mx4_token_groups(a.T, TT));
   mx4_linear_kernel<XT, TT, RB, KS><<<grid, MX4_WAVES * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
-int64_t mx4_token_groups(const Mx4Args& a, int TT) { return (a.T + TT * 16 - 1) / (TT * 16); }
-
-template <int XT, int TT, int RB>
-hipError_t launch_rb(const Mx4Args& a, hipStream_t s) {
-  // Waves that split k cost a join, and idle beyond the blocks of columns; they take rows
-  // instead while that leaves enough workgroups (65536 x 256, one token: 3.9 against 5.3 us;
-  // 65536 x 2048, 64 tokens in 8 bits: 28 against 33).
-  constexpr int64_t ENOUGH = TT > 1 ? 256 : 512;
-  const int64_t blocks = a.d.nb * mx4_token_groups(a, TT);
-  int ks = MX4_WAVES;
-  while (ks > 2 && blocks * ks / (2 * RB * MX4_WAVES) >= ENOUGH) ks /= 2;
-  if (ks == 8) return launch_ks<XT, TT, RB, 8>(a, s);
-  if (ks == 4) return launch_ks<XT, TT, RB, 4>(a, s);
-  return launch_ks<XT, TT, RB, 2>(a, s);
-}
-
-// Estimated time of a tile shape, in units of a wave's work on one block of 16 rows, 128 columns
-// and up to 32 tokens: per block of columns that on the tokens (loads, conversions) and on RB
-// blocks of weights, for as many workgroups as a CU gets, and for every workgroup (for every
-// two where two fit at once) the 10 units, 2 us, that its loads and its join take to pass.  Three
-// and four tiles of tokens cost 1.35 and 1.7 times two (the weights are expanded once), and 13 and
-// 16 units.  Fitted to sweeps of RB and TT over N 2048 .. 65536, K 256 .. 8192.
-template <int XT, int TT, int RB>
-double mx4_cost(const Mx4Args& a) {
-  const double tokens = XT == SFFN_F32 ? 4.0 : TT == 1 ? 2.2 : XT == SFFN_BF16 ? 3.0 : 1.5;
-  const int64_t groups = (a.d.nb * mx4_token_groups(a, TT) + RB - 1) / RB, n = (groups + 255) / 256;
-  const int64_t turns = mx4_pairs<XT, TT, RB>() ? (n + 1) / 2 : n;
-  const double blocks = a.d.kb > MX4_WAVES ? (double)a.d.kb / MX4_WAVES : 1.0;
-  const double more = TT > 2 ? TT - 2 : 0;
-  return (10.0 + 3.0 * more) * (double)turns +
-         (double)n * blocks * (tokens + RB) * (1.0 + 0.35 * more);
-}
-template <int XT, int TT>
-double mx4_best(const Mx4Args& a, int* rb) {
-  const double c[4] = {mx4_cost<XT, TT, 1>(a), mx4_cost<XT, TT, 2>(a), mx4_cost<XT, TT, 3>(a),
-                       mx4_cost<XT, TT, 4>(a)};
-  *rb = 1;
-  for (int i = 2; i <= 4; ++i)
-    if (c[i - 1] < c[*rb - 1]) *rb = i;
-  return c[*rb - 1];
-}
-
-// The row blocks with the least estimated time.  Measured, RB 1 / 2 / 4: one token, K 2048: N 2048
-// 3.0 / 3.4 / 4.2 us, 8192 4.0 / 3.6 / 4.3; 64 tokens in 8 bits (TT 2), RB 1 / 2 / 3 / 4: N 8192 8.0 /
-// 6.3 / 7.9 / 6.1, 9216 (K 2304) 10.6 / 10.3 / 8.0 / 10.7.
-template <int XT, int TT>
-hipError_t launch_tt(const Mx4Args& a, int rb, hipStream_t s) {
-  switch (rb) {
-    case 1: return launch_rb<XT, TT, 1>(a, s);
-    case 2: return launch_rb<XT, TT, 2>(a, s);
-    case 3: return launch_rb<XT, TT, 3>(a, s);
-    default: return launch_rb<XT, TT, 4>(a, s);
-  }
-}
-
-template <int XT>
-hipError_t launch_x(const Mx4Args& a, hipStream_t s) {
-  int rb = 1, rb_all = 1;
-  if (a.T <= 16) {
-    mx4_best<XT, 1>(a, &rb);
-    return launch_tt<XT, 1>(a, rb, s);
-  }
-  const double two = mx4_best<XT, 2>(a, &rb);
-  if constexpr (XT != SFFN_F32) {  // (more than two tiles of fp32 tokens would not fit the LDS)
-    // All tokens at once read and expand the weights once: 32768 x 2048 with 64 in 8 bits 16 us, 18
-    // in two halves; the halves fill the GPU better for fewer rows: 9216 x 2304 8.7 and 8.0.
-    if (a.T > 48) {
-      if (mx4_best<XT, 4>(a, &rb_all) < two) return launch_tt<XT, 4>(a, rb_all, s);
-    } else if (a.T > 32) {
-      if (mx4_best<XT, 3>(a, &rb_all) < two) return launch_tt<XT, 3>(a, rb_all, s);
+// I: one of the 4 x 4 x 3 forms, launched if it is f.
+template <int XT, int I>
+bool launch_if(const Mx4Args& a, const Mx4Shape& f, hipStream_t s, hipError_t* e) {
+  constexpr int TT = I / 12 + 1, RB = I / 3 % 4 + 1, KS = 2 << I % 3;
+  if constexpr (mx4_built(XT, TT, RB, KS)) {
+    if (f.tt == TT && f.rb == RB && f.ks == KS) {
+      *e = launch_form<XT, TT, RB, KS>(a, s);
+      return true;
     }
   }
-  return launch_tt<XT, 2>(a, rb, s);
+  return false;
+}
+template <int XT, int... I>
+hipError_t launch_x(const Mx4Args& a, hipStream_t s, std::integer_sequence<int, I...>) {
+  const Mx4Shape f = mx4_shape(XT, a.d.nb, a.d.kb, a.T);
+  hipError_t e = hipErrorInvalidValue;
+  (void)(launch_if<XT, I>(a, f, s, &e) || ...);
+  return e;
 }
 
 // ------------------------------------------------------------------ weights
@@ -498,10 +437,11 @@ __global__ __launch_bounds__(256) void mx4_tile_kernel(const uint8_t* codes, con
 }  // namespace
 
 hipError_t launch_mx4_linear(const Mx4Args& a, hipStream_t s) {
+  const auto forms = std::make_integer_sequence<int, 48>();
   switch (a.x_dtype) {
-    case SFFN_BF16: return launch_x<SFFN_BF16>(a, s);
-    case SFFN_F32: return launch_x<SFFN_F32>(a, s);
-    default: return launch_x<SFFN_E4M3>(a, s);
+    case SFFN_BF16: return launch_x<SFFN_BF16>(a, s, forms);
+    case SFFN_F32: return launch_x<SFFN_F32>(a, s, forms);
+    default: return launch_x<SFFN_E4M3>(a, s, forms);
   }
 }
 

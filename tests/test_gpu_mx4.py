@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_helpers import need_gpu
+from tests.mx4_forms import FORMS
 from tests.ops_helpers import rounded_from
 
 pytestmark = pytest.mark.gpu
@@ -311,3 +312,43 @@ def test_replaced_tensors():
     for name in ("tiled", "in_features", "out_features", "device"):
         with pytest.raises(AttributeError):
             setattr(lin, name, getattr(lin, name))
+
+
+def _decode_on_gpu(torch, codes, scales, K):
+    """_decode, for weights that are large on the host."""
+    c = torch.stack((codes & 15, codes >> 4), 2).view(codes.shape[0], -1).long()
+    w = torch.from_numpy(E2M1).cuda()[c]
+    return (w * torch.exp2(scales.double() - 127).repeat_interleave(32, 1))[:, :K]
+
+
+@pytest.mark.parametrize("kind,T,N,K,form", FORMS)
+def test_every_form(kind, T, N, K, form):
+    """Every kernel form of the product, every result against 64 bits; bf16 results and the ReLU are
+    those of the same sums."""
+    torch, sffn = need_gpu()
+    G = -(-K // 32)
+    gen = torch.Generator(device="cuda").manual_seed(N + K + T)
+    codes = torch.randint(0, 256, (N, 16 * G), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(118, 124, (N, G), generator=gen, device="cuda", dtype=torch.uint8)
+    x = torch.randn((T, K), generator=gen, device="cuda")
+    sc = None
+    if kind == "fp8":
+        sc = x.abs().amax(1) / 448
+        x = x / sc[:, None]
+    x = x.to({"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}[kind])
+    bias = torch.randn(N, generator=gen, device="cuda")
+    lin = sffn.Mx4Linear(codes, scales, bias=bias, in_features=K)
+    y = lin(x, x_scale=sc, dtype=torch.float32)
+    x64, s64 = x.float().double(), 1.0 if sc is None else sc.double()[:, None]
+    step = max(1, (1 << 27) // K)
+    for i in range(0, N, step):
+        W = _decode_on_gpu(torch, codes[i:i + step], scales[i:i + step], K)
+        b = bias[i:i + step].double()
+        z = (x64 @ W.t()) * s64 + b
+        size = (x64.abs() @ W.abs().t()) * s64 + b.abs()
+        off = (y[:, i:i + step].double() - z).abs()
+        assert bool((off <= (K + 20) * 2.0 ** -23 * size + 1e-30).all()), (i, float((off / size).max()))
+        del W, z, size, off
+    assert torch.equal(lin(x, x_scale=sc, dtype=torch.bfloat16), y.to(torch.bfloat16))
+    lin.relu = True
+    assert torch.equal(lin(x, x_scale=sc, dtype=torch.float32), y.clamp_min(0))
