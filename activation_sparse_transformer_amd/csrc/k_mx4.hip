@@ -3,11 +3,12 @@
 //
 // One wave holds 16 x 128 weights in a 16-byte load a lane (the tiled layout: 1 KB contiguous),
 // expands them to bf16 with the packed conversion that applies the scale (exact: a bf16 holds
-// e2m1 times a power of two) and multiplies on the matrix cores: A = 16 weight rows, B = up to
-// 16 tokens, v_mfma_f32_16x16x32_bf16, four for a block.  Token types: bf16 as it is; e4m3
-// widened to bf16 (exact); fp32 as the sum of three bf16 (truncations: 8 + 8 + 8 bits, exact),
-// three products.  (The scaled 8-bit x 4-bit matrix instruction would need no expansion, but its
-// sums over 128 columns came out up to 1e-4 of the absolute products off; these are fp32.)
+// e2m1 times a power of two, from the smallest, 2^-128, to 2^128, where it overflows) and
+// multiplies on the matrix cores: A = 16 weight rows, B = up to 16 tokens,
+// v_mfma_f32_16x16x32_bf16, four for a block.  Token types: bf16 as it is; e4m3 widened to bf16
+// (exact); fp32 as the sum of three bf16 (truncations: 8 + 8 + 8 bits, exact), three products.
+// (The scaled 8-bit x 4-bit matrix instruction would need no expansion, but its sums over 128
+// columns came out up to 1e-4 of the absolute products off; these are fp32.)
 // The waves of a workgroup split k and add their fp32 sums in LDS in wave order.
 //
 // Bound by reading the weights at few tokens: 65536 x 8192 at 4 tokens 50.2 us (5.7 TB/s); at 64

@@ -102,9 +102,13 @@ sffn_status_t sffn_mx4_tile(const uint8_t *codes, const uint8_t *scales, int32_t
  * x [T, K] is SFFN_BF16, SFFN_F32 or SFFN_E4M3; x_scale [T] fp32 multiplies a token's results
  * (required for SFFN_E4M3, otherwise it may be NULL).  bias [N] fp32 may be NULL.  act is
  * max(., 0) if relu is nonzero (NaN stays).  y [T, N] (stride N) is SFFN_F32 or SFFN_BF16.
- * Products are exact, sums in fp32.  N up to 2^26, K up to 2^30, N K below 2^36.  Every T up to
- * 2^20 is accepted; the kernel is made
- * for T <= 64, and reads the weights again for every further 64 tokens. */
+ * Products are exact and sums in fp32, within fp32's range: a weight of 2^128 or more (scales 253
+ * and 254 with a large code, which sffn_mx4_quantize never writes) makes its row's results not
+ * finite, also where a small token value would bring the product back.
+ * N up to 2^26, K up to 2^30, N K below 2^36.  Every T up to 2^20 is accepted; the kernel is made
+ * for T <= 64.  Up to 16 tokens read the weights once, more read them again for every 32 tokens, or
+ * with SFFN_BF16 and SFFN_E4M3 tokens for every 64 where that is estimated to be quicker (33 to
+ * 64 tokens: once). */
 sffn_status_t sffn_mx4_linear(const void *tiled, int32_t N, int32_t K, int32_t x_dtype,
                               const void *x, int64_t x_stride, const float *x_scale, int32_t T,
                               const float *bias, int32_t relu, int32_t y_dtype, void *y,

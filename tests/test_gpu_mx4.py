@@ -352,3 +352,53 @@ def test_every_form(kind, T, N, K, form):
     assert torch.equal(lin(x, x_scale=sc, dtype=torch.bfloat16), y.to(torch.bfloat16))
     lin.relu = True
     assert torch.equal(lin(x, x_scale=sc, dtype=torch.float32), y.clamp_min(0))
+
+
+@pytest.mark.parametrize("T,N,K,kind", [(7, 8192, 2048, "fp8"), (64, 9216, 2304, "fp8"), (48, 8192, 2048, "bf16"),
+                                        (16, 6144, 1536, "f32"), (33, 2048, 512, "f32")])
+def test_one_token_alone_and_among_others(T, N, K, kind):
+    """A token's result alone and in a batch: both within the bound of a product from the exact one,
+    element by element, so within twice that of each other."""
+    torch, sffn = need_gpu()
+    rng = np.random.default_rng(T + N)
+    codes, scales = _weights(rng, N, K)
+    x, sc = _tokens(torch, rng, T, K, kind)
+    lin = sffn.Mx4Linear(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    y = lin(x, x_scale=sc, dtype=torch.float32).cpu().double().numpy()
+    size = np.abs(x.float().cpu().double().numpy()) @ np.abs(_decode(codes, scales, K)).T
+    if sc is not None:
+        size = size * sc.cpu().double().numpy()[:, None]
+    for t in (0, T // 2, T - 1):
+        one = lin(x[t:t + 1], x_scale=None if sc is None else sc[t:t + 1], dtype=torch.float32)
+        off = np.abs(one.cpu().double().numpy()[0] - y[t])
+        assert np.all(off <= 2 * ((K + 20) * 2.0 ** -23 * size[t] + 1e-30))
+
+
+@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+def test_every_scale(T, kind):
+    """Every code under every scale, times a token value that brings the product into fp32's range: the
+    exact product, down to the smallest (subnormal) weights.  Weights of 2^128 and more (scales 253 and
+    254) are beyond fp32's range, and their rows not finite."""
+    torch, sffn = need_gpu()
+    K, N = 32, 16 * 255
+    codes = np.zeros((N, K // 2), np.uint8)
+    codes[:, 0] = np.arange(N) % 16
+    s = np.arange(N) // 16
+    lin = sffn.Mx4Linear(torch.from_numpy(codes).cuda(), torch.from_numpy(s.astype(np.uint8)[:, None]).cuda())
+    w = np.ldexp(E2M1[codes[:, 0]], s - 127)
+    for power, rows in ((60, s <= 150), (-60, s >= 100)):
+        x = torch.zeros((T, K), device="cuda")
+        sc = None
+        x[:, 0] = 2.0 ** power
+        if kind == "fp8":  # the token's scale brings it
+            x[:, 0] = 1.0
+            sc = torch.full((T,), 2.0 ** power, device="cuda")
+        x = x.to({"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}[kind])
+        y = lin(x, x_scale=sc, dtype=torch.float32).cpu().double().numpy()
+        want = np.ldexp(w, power)
+        if kind == "fp8":  # the sum before the token's scale is fp32 too
+            rows = rows & (np.abs(w) >= 2.0 ** -126) | rows & (w == 0)
+        fits = np.abs(w) < 2.0 ** 128
+        assert np.array_equal(y[:, rows & fits], np.broadcast_to(want, y.shape)[:, rows & fits])
+        assert not np.isfinite(y[:, ~fits]).any()
