@@ -23,7 +23,7 @@ namespace {
 template <bool NT>
 __device__ __forceinline__ void store4(float* p, const float* v, int n) {
   if (n >= 4) {
-    store_v<NT>(reinterpret_cast<f32x4_a4*>(p), f32x4{v[0], v[1], v[2], v[3]});
+    store_v<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -33,7 +33,7 @@ __device__ __forceinline__ void store4(float* p, const float* v, int n) {
 template <bool NT>
 __device__ __forceinline__ void store4(uint16_t* p, const float* v, int n) {
   if (n >= 4) {
-    store_v<NT>(reinterpret_cast<u32x2_a2*>(p),
+    store_v<NT>(p,
                 u32x2{(uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
                       (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16)});
   } else {
@@ -46,7 +46,7 @@ template <bool NT>
 __device__ __forceinline__ void load_codes4(const uint8_t* p, int n, float* o) {
   uint32_t q = 0;
   if (n >= 4) {
-    q = load_v<NT, uint32_t>(reinterpret_cast<const u32_a1*>(p));
+    q = load_v<NT, uint32_t>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -61,7 +61,7 @@ template <bool NT>
 __device__ __forceinline__ void store_codes4(uint8_t* p, const float* v, int n) {
   const uint32_t q = e4m3x4(v[0], v[1], v[2], v[3]);
   if (n >= 4) {
-    store_v<NT>(reinterpret_cast<u32_a1*>(p), q);
+    store_v<NT>(p, q);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

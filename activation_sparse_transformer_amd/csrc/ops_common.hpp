@@ -84,22 +84,25 @@ __device__ __forceinline__ void store8_n(T* p, const float* v, int n) {
     if (i < n) store1(p + i, v[i]);
 }
 
-// One vector access; NT: past the caches.
-template <bool NT, typename V, typename M>
-__device__ __forceinline__ V load_v(const M* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
-  else return *p;
+// One vector access at any address of its elements' alignment; NT: past the caches, at the
+// vector's own alignment.
+template <bool NT, typename V>
+__device__ __forceinline__ V load_v(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  V v;
+  __builtin_memcpy(&v, p, sizeof(v));
+  return v;
 }
-template <bool NT, typename V, typename M>
-__device__ __forceinline__ void store_v(M* p, V v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
-  else *p = v;
+template <bool NT, typename V>
+__device__ __forceinline__ void store_v(void* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else __builtin_memcpy(p, &v, sizeof(v));
 }
 // Four consecutive elements, of which the first n exist.
 template <bool NT>
 __device__ __forceinline__ void load4(const float* p, int n, float* o) {
   if (n >= 4) {
-    const f32x4 v = load_v<NT, f32x4>(reinterpret_cast<const f32x4_a4*>(p));
+    const f32x4 v = load_v<NT, f32x4>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = v[i];
   } else {
@@ -111,7 +114,7 @@ template <bool NT>
 __device__ __forceinline__ void load4(const uint16_t* p, int n, float* o) {
   u32x2 v = u32x2{0, 0};
   if (n >= 4) {
-    v = load_v<NT, u32x2>(reinterpret_cast<const u32x2_a2*>(p));
+    v = load_v<NT, u32x2>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

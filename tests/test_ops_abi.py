@@ -237,3 +237,14 @@ def test_adamw_overlap(ops, kw, bits):
     h = ops.AdamwHyperC(**HYPER)
     assert ops._lib().sffn_adamw_step(ctypes.byref(t), 1, BF16, F32, bits, ctypes.byref(h), None, None) == INVALID
     assert "overlap" in _message()
+
+
+@pytest.mark.parametrize("name", ["k_adamw", "k_rms_norm", "k_rms_norm_grad", "k_mx4"])
+def test_vector_accesses_are_declared_at_their_alignment(name):
+    """Vector accesses to memory of an element's alignment are written as such (a type's lower
+    alignment is lost in a template argument, and the compiler may then rely on the vector's)."""
+    import subprocess
+    from activation_sparse_transformer_amd import build
+    r = subprocess.run([build.HIPCC, *build.FLAGS, "-Werror=align-mismatch", "-fsyntax-only", "--cuda-device-only",
+                        os.path.join(build.CSRC, name + ".hip")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
