@@ -111,8 +111,8 @@ __device__ __forceinline__ void adamw_part(const AdamwTable& tab, const sffn_ada
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool in = i < n;  // past the end: codes 0 and gradient 0, but the scale may be anything
-      bm = in ? MaxNan()(bm, fabsf(m[i])) : bm;
-      br = in ? MaxNan()(br, root[i]) : br;
+      bm = in ? max_abs(bm, m[i]) : bm;
+      br = in ? max_abs(br, root[i]) : br;
     }
     bm = lane_reduce<64>(bm, MaxNan()) / E4M3_MAX;
     br = lane_reduce<64>(br, MaxNan()) / E4M3_MAX;

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(L > 256 ? 1024 : 256) void rms_norm_kernel(NormArgs
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       h[v][i] = h[v][i] * rstd * rg[v].get(i);
-      if (FP8) big = MaxNan()(big, fabsf(h[v][i]));
+      if (FP8) big = max_abs(big, h[v][i]);
     }
   float stat = rstd;
   if constexpr (FP8) {
