@@ -240,7 +240,8 @@ struct Mx4Weights {
 // KS of a workgroup's waves split k, the others take further rows.  Rows past the end are read as
 // the last one and not stored; what a column without a token holds is not stored either (a
 // product's columns do not mix).  More than 16 tokens are turned in LDS; up to 16 each lane loads
-// its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048).
+// its own (one token is then one access a group of lanes: 3.6 against 3.9 us at 8192 x 2048,
+// launches one after another; 4.2 in a trace).
 // Many waves hide the loads: a second block of columns in flight in a wave gained nothing.
 template <int XT, int TT, int RB, int KS>
 __global__ __launch_bounds__(MX4_WAVES * 64, (mx4_pairs(XT, TT, RB) ? 4 : 2)) void

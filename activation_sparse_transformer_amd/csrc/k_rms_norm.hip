@@ -5,8 +5,9 @@
 //
 // One pass: a row's elements stay in the registers of the L lanes that loaded them (NV vectors
 // of 8 a lane) between the sum of squares and the output, so x and the residual are read once
-// and h, y written once.  Bound by memory: 16384 x 2304 bf16 with the residual moves 302 MB in
-// 53 us (5.7 TB/s; a copy reaches 4.8), with 8 bits out 264 MB in 48 us.
+// and h, y written once.  Bound by memory: 8192 x 2048 bf16 with the residual moves 134 MB in 22.4 us
+// (6.0 TB/s; a copy reaches 4.8), 16384 x 2304 with 8 bits out 264 MB in 44 us (from a trace; calls
+// one after another take 24.6 and 48).
 #include "ops_common.hpp"
 
 namespace sffn {

@@ -7,7 +7,8 @@
 // dgain in registers too; a workgroup joins its row groups in LDS in a fixed order and writes
 // one partial row, and a second kernel adds the partial rows in order (no atomics: the result
 // depends on the sizes alone).  Bound by memory: 16384 x 2304 bf16 with dres moves 302 MB in
-// 57 us (5.3 TB/s), the second kernel takes 3.  (Loading a lane's next row before this one is
+// 55 us (5.5 TB/s), the second kernel takes 4.8 (from a trace).  Above 16384 columns a lane's arrays no
+// longer fit its 128 registers and spill: 1024 x 32768 takes 186 us for 270 MB.  (Loading a lane's next row before this one is
 // reduced helped 8192 x 4096 by 3 us and cost 16384 x 2304 as much.)
 #include "ops_common.hpp"
 
