@@ -408,14 +408,13 @@ class Mx4Linear:
 class AdamW:
     """AdamW over a list of tensors, updated in place by one launch (per 48 tensors).
 
-    params: contiguous device tensors, all float32 or all bfloat16; none of the tensors that are
-    updated may overlap another.  master: their float32
+    params: contiguous device tensors, all float32 or all bfloat16.  master: their float32
     copies (for bfloat16 params), the values the step is taken on; params then receive the
     rounded result.  state_bits 32 keeps both moments in float32; 8 keeps the first moment and
     the root of the second as float8_e4m3fn with one float32 scale per 256 elements.  `state`
     continues from given tensors instead of zeros: [m, v] or [m, m_scale, r, r_scale], each a
     list like params; with it, state_bits goes by its length, and `step` is the number of steps
-    done.
+    done.  A step writes all of these tensors: none may overlap another.
 
     The tensors are in `.params`, `.master` and `.state`, in that order, as tuples: to replace
     some, assign the whole (checked as here); a tensor whose storage was replaced (p.data = q)
