@@ -15,5 +15,6 @@ from .sparse_ffn import (  # noqa: F401
     MAX_TILES,
 )
 from .ffn_ops import (  # noqa: F401
-    rms_norm, rms_norm_fp8, rms_norm_backward, mx4_quantize, Mx4Linear, AdamW,
+    rms_norm, rms_norm_fp8, rms_norm_backward, layer_norm, layer_norm_fp8, layer_norm_backward,
+    mx4_quantize, Mx4Linear, AdamW,
 )

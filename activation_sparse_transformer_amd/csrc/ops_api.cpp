@@ -80,6 +80,42 @@ sffn_status_t check_overlap(const Rows (&out)[N], const Rows (&in)[M]) {
   return SFFN_OK;
 }
 
+// What both norms check of their arguments; `bias` and `mean` are null where a norm has none.
+sffn_status_t check_norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_stride,
+                         const void* residual, int64_t residual_stride, const void* gain,
+                         const void* bias, int64_t rows, int32_t d, const void* y,
+                         const float* mean, const float* stat, const void* h, bool fp8) {
+  OPS_TRY(check_matrix(x, x_stride, rows, d, dtype, "x is NULL", "x_stride is less than d"));
+  if (residual)
+    OPS_TRY(check_matrix(residual, residual_stride, rows, d, dtype, "residual is NULL",
+                         "residual_stride is less than d"));
+  if (!gain || !y) return invalid("gain or the output is NULL");
+  if (fp8 && !stat) return invalid("scale is NULL");
+  if (misaligned(gain, size_of(gain_dtype)) || misaligned(bias, size_of(gain_dtype)) ||
+      misaligned(y, fp8 ? 1 : size_of(dtype)) || misaligned(h, size_of(dtype)) ||
+      misaligned(mean, 4) || misaligned(stat, 4))
+    return invalid("a pointer is not aligned to its element");
+  const size_t size = size_of(dtype);
+  const Rows xr = matrix(x, x_stride, rows, d, size),
+             rr = matrix(residual, residual_stride, rows, d, size),
+             yr = block(y, (uint64_t)rows * d * (fp8 ? 1 : size)),
+             hr = block(h, (uint64_t)rows * d * size), mr = block(mean, (uint64_t)rows * 4),
+             sr = block(stat, (uint64_t)rows * 4);
+  // a row is in registers before any of it is written, so that h, and y of the same type, may take
+  // the place of x or the residual
+  const Rows none = block(nullptr, 0), gr = block(gain, (uint64_t)d * size_of(gain_dtype)),
+             br = block(bias, (uint64_t)d * size_of(gain_dtype));
+  const auto in_place = [](const Rows& o, const Rows& i) {
+    return o.at == i.at && o.width == i.width && i.rows == 1;
+  };
+  for (const Rows* i : {&xr, &rr}) {
+    OPS_TRY(check_overlap({hr}, {in_place(hr, *i) ? none : *i}));
+    OPS_TRY(check_overlap({yr}, {!fp8 && in_place(yr, *i) ? none : *i}));
+  }
+  OPS_TRY(check_overlap({yr, hr, mr, sr}, {gr, br}));
+  return check_overlap({mr, sr}, {xr, rr});
+}
+
 sffn_status_t norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_stride,
                    const void* residual, int64_t residual_stride, const void* gain, float eps,
                    int64_t rows, int32_t d, void* y, float* stat, void* h, bool fp8,
@@ -89,39 +125,34 @@ sffn_status_t norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_s
   if (!(eps >= 0.f)) return invalid("eps must not be negative");
   if (h && !residual) return invalid("h without a residual");
   if (rows == 0) return SFFN_OK;
-  OPS_TRY(check_matrix(x, x_stride, rows, d, dtype, "x is NULL", "x_stride is less than d"));
-  if (residual)
-    OPS_TRY(check_matrix(residual, residual_stride, rows, d, dtype, "residual is NULL",
-                         "residual_stride is less than d"));
-  if (!gain || !y) return invalid("gain or the output is NULL");
-  if (fp8 && !stat) return invalid("scale is NULL");
-  if (misaligned(gain, size_of(gain_dtype)) || misaligned(y, fp8 ? 1 : size_of(dtype)) ||
-      misaligned(h, size_of(dtype)) || misaligned(stat, 4))
-    return invalid("a pointer is not aligned to its element");
-  const size_t size = size_of(dtype);
-  const Rows xr = matrix(x, x_stride, rows, d, size),
-             rr = matrix(residual, residual_stride, rows, d, size),
-             yr = block(y, (uint64_t)rows * d * (fp8 ? 1 : size)),
-             hr = block(h, (uint64_t)rows * d * size),
-             sr = block(stat, (uint64_t)rows * 4);
-  // a row is in registers before any of it is written, so that h, and y of the same type, may take
-  // the place of x or the residual
-  const Rows none = block(nullptr, 0), gr = block(gain, (uint64_t)d * size_of(gain_dtype));
-  const auto in_place = [](const Rows& o, const Rows& i) {
-    return o.at == i.at && o.width == i.width && i.rows == 1;
-  };
-  for (const Rows* i : {&xr, &rr}) {
-    OPS_TRY(check_overlap({hr}, {in_place(hr, *i) ? none : *i}));
-    OPS_TRY(check_overlap({yr}, {!fp8 && in_place(yr, *i) ? none : *i}));
-  }
-  OPS_TRY(check_overlap({yr, hr, sr}, {gr}));
-  OPS_TRY(check_overlap({sr}, {xr, rr}));
+  OPS_TRY(check_norm(dtype, gain_dtype, x, x_stride, residual, residual_stride, gain, nullptr, rows,
+                     d, y, nullptr, stat, h, fp8));
   const NormArgs a{x, x_stride, residual, residual ? residual_stride : 0, gain, eps, rows, d, y, stat, h};
   auto f = [&] {
     return launch_rms_norm(dtype == SFFN_BF16, gain_dtype == SFFN_F32, fp8, a,
                            static_cast<hipStream_t>(stream));
   };
   return api_run(fp8 ? "rms_norm_fp8" : "rms_norm", static_cast<hipStream_t>(stream), f);
+}
+
+sffn_status_t layer_norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_stride,
+                         const void* residual, int64_t residual_stride, const void* gain,
+                         const void* bias, float eps, int64_t rows, int32_t d, void* y,
+                         float* mean, float* stat, void* h, bool fp8, void* stream) {
+  OPS_TRY(check_types(dtype, gain_dtype));
+  OPS_TRY(check_rows(rows, d));
+  if (!(eps >= 0.f)) return invalid("eps must not be negative");
+  if (h && !residual) return invalid("h without a residual");
+  if (rows == 0) return SFFN_OK;
+  OPS_TRY(check_norm(dtype, gain_dtype, x, x_stride, residual, residual_stride, gain, bias, rows, d,
+                     y, mean, stat, h, fp8));
+  const LayerNormArgs a{x, x_stride, residual, residual ? residual_stride : 0, gain, bias, eps,
+                        rows, d, y, mean, stat, h};
+  auto f = [&] {
+    return launch_layer_norm(dtype == SFFN_BF16, gain_dtype == SFFN_F32, fp8, a,
+                             static_cast<hipStream_t>(stream));
+  };
+  return api_run(fp8 ? "layer_norm_fp8" : "layer_norm", static_cast<hipStream_t>(stream), f);
 }
 
 sffn_status_t check_mx4(int32_t N, int32_t K) {
@@ -204,6 +235,79 @@ sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const vo
   if (!dgain || (rows > 0 && groups == 0)) return SFFN_OK;
   auto f = [&] { return launch_rms_norm_grad_sum(part, groups, d, dgain, s); };
   return api_run("rms_norm_grad_sum", s, f);
+}
+
+sffn_status_t sffn_layer_norm(int32_t dtype, int32_t gain_dtype, const void* x, int64_t x_stride,
+                              const void* residual, int64_t residual_stride, const void* gain,
+                              const void* bias, float eps, int64_t rows, int32_t d, void* y,
+                              float* mean, float* rstd, void* h, void* stream) {
+  return layer_norm(dtype, gain_dtype, x, x_stride, residual, residual_stride, gain, bias, eps,
+                    rows, d, y, mean, rstd, h, false, stream);
+}
+
+sffn_status_t sffn_layer_norm_fp8(int32_t dtype, int32_t gain_dtype, const void* x,
+                                  int64_t x_stride, const void* residual, int64_t residual_stride,
+                                  const void* gain, const void* bias, float eps, int64_t rows,
+                                  int32_t d, void* q, float* scale, void* h, void* stream) {
+  return layer_norm(dtype, gain_dtype, x, x_stride, residual, residual_stride, gain, bias, eps,
+                    rows, d, q, nullptr, scale, h, true, stream);
+}
+
+sffn_status_t sffn_layer_norm_backward_workspace(int64_t rows, int32_t d, size_t* bytes) {
+  OPS_TRY(check_rows(rows, d));
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = (size_t)layer_norm_grad_parts(rows, d) * 2 * d * sizeof(float);
+  return SFFN_OK;
+}
+
+sffn_status_t sffn_layer_norm_backward(int32_t dtype, int32_t gain_dtype, const void* dy,
+                                       int64_t dy_stride, const void* h, int64_t h_stride,
+                                       const void* gain, const float* mean, const float* rstd,
+                                       const void* dres, int64_t dres_stride, int64_t rows,
+                                       int32_t d, void* dx, float* dgain, float* dbias,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  OPS_TRY(check_types(dtype, gain_dtype));
+  OPS_TRY(check_rows(rows, d));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool sums = dgain || dbias;
+  const int parts = sums ? layer_norm_grad_parts(rows, d) : 0;
+  const size_t need = (size_t)parts * 2 * d * sizeof(float);
+  float* part = parts > 0 ? static_cast<float*>(workspace) : nullptr;
+  if (misaligned(dgain, 4) || misaligned(dbias, 4))
+    return invalid("a pointer is not aligned to its element");
+  const Rows dgr = block(dgain, (uint64_t)d * 4), dbr = block(dbias, (uint64_t)d * 4);
+  if (rows > 0) {
+    OPS_TRY(check_matrix(dy, dy_stride, rows, d, dtype, "dy is NULL", "dy_stride is less than d"));
+    OPS_TRY(check_matrix(h, h_stride, rows, d, dtype, "h is NULL", "h_stride is less than d"));
+    if (dres)
+      OPS_TRY(check_matrix(dres, dres_stride, rows, d, dtype, "dres is NULL",
+                           "dres_stride is less than d"));
+    if (!gain || !mean || !rstd || !dx) return invalid("gain, mean, rstd or dx is NULL");
+    if (misaligned(gain, size_of(gain_dtype)) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+        misaligned(dx, size_of(dtype)))
+      return invalid("a pointer is not aligned to its element");
+    if (parts > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+      return invalid("workspace is NULL, misaligned or too small");
+    const size_t size = size_of(dtype);
+    const Rows dxr = block(dx, (uint64_t)rows * d * size), wr = block(part, need),
+               dyr = matrix(dy, dy_stride, rows, d, size), hr = matrix(h, h_stride, rows, d, size),
+               gr = block(gain, (uint64_t)d * size_of(gain_dtype)),
+               mr = block(mean, (uint64_t)rows * 4), sr = block(rstd, (uint64_t)rows * 4),
+               rr = matrix(dres, dres_stride, rows, d, size);
+    OPS_TRY(check_overlap({dxr, dgr, dbr, wr}, {dyr, hr, gr, mr, sr}));
+    OPS_TRY(check_overlap({dgr, dbr, wr}, {rr}));
+    if (dx != dres || rr.rows > 1) OPS_TRY(check_overlap({dxr}, {rr}));
+    const LayerNormGradArgs a{dy, dy_stride, h, h_stride, gain, mean, rstd, dres,
+                              dres ? dres_stride : 0, rows, d, dx, dgain, dbias, part, 0};
+    auto f = [&] { return launch_layer_norm_grad(dtype == SFFN_BF16, gain_dtype == SFFN_F32, a, s); };
+    OPS_TRY(api_run("layer_norm_grad", s, f));
+    if (parts == 0) return SFFN_OK;
+  } else {
+    if (!sums) return SFFN_OK;
+    if (overlap(dgr, dbr)) return invalid("two outputs overlap");
+  }
+  auto f = [&] { return launch_layer_norm_grad_sum(part, parts, d, dgain, dbias, s); };
+  return api_run("layer_norm_grad_sum", s, f);
 }
 
 sffn_status_t sffn_mx4_quantize(int32_t dtype, const void* W, int64_t w_stride, int32_t N,

@@ -197,6 +197,26 @@ __device__ __forceinline__ float row_reduce(float v, Op op, float* red) {
   }
   return v;
 }
+// Sums of two values over the L lanes of a row, with one barrier.
+template <int L>
+__device__ __forceinline__ void row_reduce2(float& a, float& b, float* red_a, float* red_b) {
+  a = lane_reduce<(L < 64 ? L : 64)>(a, Add());
+  b = lane_reduce<(L < 64 ? L : 64)>(b, Add());
+  if constexpr (L > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      red_a[threadIdx.x >> 6] = a;
+      red_b[threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = red_a[0];
+    b = red_b[0];
+#pragma unroll
+    for (int i = 1; i < L / 64; ++i) {
+      a += red_a[i];
+      b += red_b[i];
+    }
+  }
+}
 // Quotients of values up to 448 s by a positive scale s, bit for bit the divide's: the product with
 // the rounded reciprocal is a few roundings off, and one fma with its remainder corrects it
 // (P. Markstein, 1990; compared with the divide on 3.2e9 pairs, half of them next to the middle
@@ -301,6 +321,51 @@ hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a,
 // dgain[c] = sum of the n partial rows (0 with none)
 hipError_t launch_rms_norm_grad_sum(const float* part, int n, int32_t d, float* dgain,
                                     hipStream_t s);
+
+struct LayerNormArgs {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t residual_stride;
+  const void* gain;
+  const void* bias;
+  float eps;
+  int64_t rows;
+  int32_t d;
+  void* y;      // dtype, or e4m3 bytes
+  float* mean;
+  float* stat;  // rstd, or the 8-bit scales
+  void* h;
+};
+hipError_t launch_layer_norm(bool bf16, bool gain_f32, bool fp8, const LayerNormArgs& a,
+                             hipStream_t s);
+
+struct LayerNormGradArgs {
+  const void* dy;
+  int64_t dy_stride;
+  const void* h;
+  int64_t h_stride;
+  const void* gain;
+  const float* mean;
+  const float* rstd;
+  const void* dres;
+  int64_t dres_stride;
+  int64_t rows;
+  int32_t d;
+  void* dx;
+  float* dgain;
+  float* dbias;
+  float* part;    // [layer_norm_grad_parts(rows, d), 2, d] partial sums of dgain and dbias, or null
+  int sum_parts;  // the launcher's
+};
+// Partial rows of dgain and dbias, whose sum takes a second kernel; 0 where the first one writes the
+// sums themselves.
+int layer_norm_grad_parts(int64_t rows, int32_t d);
+hipError_t launch_layer_norm_grad(bool bf16, bool gain_f32, const LayerNormGradArgs& a,
+                                  hipStream_t s);
+// dgain[c] and dbias[c] = sums of the n partial rows (0 with none); either may be null
+hipError_t launch_layer_norm_grad_sum(const float* part, int n, int32_t d, float* dgain,
+                                      float* dbias, hipStream_t s);
 
 // The tiled 4-bit layout: for every 16 rows and 128 columns a block of MX4_BLOCK bytes: 1 KB of
 // codes (lane l of a wave: row l % 16, word j of its four: columns 32 j + 8 (l / 16) and the

@@ -1,5 +1,6 @@
-"""Binding of the operators around the sparse FFN layer (the C ABI in include/ffn_ops.h): the
-RMS norm with the residual's sum and its gradient, products with 4-bit weights, AdamW.
+"""Binding of the operators around the sparse FFN layer (the C ABI in include/ffn_ops.h): the RMS
+norm and the layer norm with the residual's sum, their gradients, products with 4-bit weights, the
+norm of all gradients and clipping by it, AdamW.
 
 Argument marshalling only, as in ``sparse_ffn``: every step runs in the library's HIP kernels;
 PyTorch supplies device memory and the stream.  With ``stream=None`` a call runs on PyTorch's
@@ -46,12 +47,18 @@ _GRAD_WORD = AdamwTensorC.grad.offset // 8
 _SHAPE, _DTYPE = attrgetter("shape"), attrgetter("dtype")
 
 _NORM = [_I32, _I32, _P, _I64, _P, _I64, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _P]
+_LAYER_NORM = _NORM[:7] + [_P] + _NORM[7:]
 _PROTOS = {
     "sffn_rms_norm": _NORM,
     "sffn_rms_norm_fp8": _NORM,
     "sffn_rms_norm_backward_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
     "sffn_rms_norm_backward": [_I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I32, _P,
                                _P, _P, _SZ, _P],
+    "sffn_layer_norm": _LAYER_NORM[:-1] + [_P, _P],
+    "sffn_layer_norm_fp8": _LAYER_NORM,
+    "sffn_layer_norm_backward_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
+    "sffn_layer_norm_backward": [_I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I32,
+                                 _P, _P, _P, _P, _SZ, _P],
     "sffn_mx4_quantize": [_I32, _P, _I64, _I32, _I32, _P, _P, _P],
     "sffn_mx4_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
     "sffn_mx4_tile": [_P, _P, _I32, _I32, _P, _P],
@@ -278,6 +285,127 @@ def _norm_workspace(rows, d):
     st = _lib().sffn_rms_norm_backward_workspace(rows, d, ctypes.byref(n))
     if st:
         _fail(st, "sffn_rms_norm_backward_workspace")
+    return n.value
+
+
+def _layer_norm(name, x, gain, bias, residual, eps, y, mean, stat, h, stream):
+    f = _lib()
+    torch = f.torch
+    dev, dt = x.device, x.dtype
+    if _elsewhere(f, dev, stream):
+        with _on(dev, stream, x, gain, bias, residual, y, mean, stat, h):
+            return _layer_norm(name, x, gain, bias, residual, eps, y, mean, stat, h, None)
+    fp8 = name == "sffn_layer_norm_fp8"
+    shape = x.shape
+    if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape
+    xs = d if x.is_contiguous() else _matrix(x, "x", dt, shape, dev)
+    rs = _matrix(residual, "residual", dt, shape, dev) if residual is not None else 0
+    if gain.dtype != dt and gain.dtype != torch.float32:
+        raise ValueError("gain must have x's type or float32")
+    _plain(gain, "gain", gain.dtype, (d,), dev)
+    if bias is not None:
+        _plain(bias, "bias", gain.dtype, (d,), dev)
+    out_t = torch.float8_e4m3fn if fp8 else dt
+    if y is not None:
+        _plain(y, "q" if fp8 else "y", out_t, shape, dev)
+    else:
+        y = x.new_empty(shape, dtype=out_t) if fp8 or xs != d else torch.empty_like(x)
+    stat = x.new_empty(rows, dtype=torch.float32) if stat is None else \
+        _plain(stat, "scale" if fp8 else "rstd", torch.float32, (rows,), dev)
+    if not fp8:
+        mean = torch.empty_like(stat) if mean is None else \
+            _plain(mean, "mean", torch.float32, (rows,), dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only with a residual")
+    else:
+        if h is not None:
+            _plain(h, "h", dt, shape, dev)
+        else:
+            h = torch.empty_like(residual) if rs == d else residual.new_empty(shape)
+    stats = (stat.data_ptr(),) if fp8 else (mean.data_ptr(), stat.data_ptr())
+    st = getattr(f, name)(f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs,
+                          gain.data_ptr(), _ptr(bias), eps, rows, d, y.data_ptr(), *stats, _ptr(h),
+                          f.stream(dev.index))
+    if st:
+        _fail(st, name)
+    return y, x if residual is None else h, mean, stat
+
+
+def layer_norm(x, gain, bias=None, residual=None, eps=1e-5, y=None, h=None, mean=None, rstd=None,
+               stream=None):
+    """h = x + residual, mean and rstd = 1 / sqrt(var + eps) of its rows, y = (h - mean) * rstd *
+    gain + bias over the rows of x [rows, d] (float32 or bfloat16; rows may be strided).  gain [d]
+    has x's type or float32, bias [d] gain's type.  Returns (y, h, mean, rstd): what
+    layer_norm_backward takes; h is x without a residual.  Outputs may be given as in rms_norm."""
+    return _layer_norm("sffn_layer_norm", x, gain, bias, residual, eps, y, mean, rstd, h, stream)
+
+
+def layer_norm_fp8(x, gain, bias=None, residual=None, eps=1e-5, q=None, scale=None, h=None,
+                   stream=None):
+    """The layer norm for serving, its output in 8 bits as rms_norm_fp8 gives it.  Returns
+    (q, scale, h)."""
+    q, h, _, scale = _layer_norm("sffn_layer_norm_fp8", x, gain, bias, residual, eps, q, None,
+                                 scale, h, stream)
+    return q, scale, h
+
+
+def layer_norm_backward(dy, h, gain, mean, rstd, dres=None, with_dgain=True, with_dbias=True,
+                        dx=None, dgain=None, dbias=None, stream=None):
+    """Gradient of layer_norm for dL/dy = dy, with the forward's h, mean and rstd.  Returns
+    (dx, dgain, dbias): dx, in h's type, is the gradient of both x and the residual; dgain and
+    dbias are float32, or None if they are not wanted.  dres and given outputs are as in
+    rms_norm_backward."""
+    f = _lib()
+    torch = f.torch
+    dev, dt = h.device, h.dtype
+    if _elsewhere(f, dev, stream):
+        with _on(dev, stream, dy, h, gain, mean, rstd, dres, dx, dgain, dbias):
+            return layer_norm_backward(dy, h, gain, mean, rstd, dres, with_dgain, with_dbias, dx,
+                                       dgain, dbias)
+    shape = h.shape
+    if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("h must be a float32 or bfloat16 tensor [rows, d]")
+    rows, d = shape
+    hs = d if h.is_contiguous() else _matrix(h, "h", dt, shape, dev)
+    ys = _matrix(dy, "dy", dt, shape, dev)
+    rs = _matrix(dres, "dres", dt, shape, dev) if dres is not None else 0
+    if gain.dtype != dt and gain.dtype != torch.float32:
+        raise ValueError("gain must have h's type or float32")
+    _plain(gain, "gain", gain.dtype, (d,), dev)
+    _plain(mean, "mean", torch.float32, (rows,), dev)
+    _plain(rstd, "rstd", torch.float32, (rows,), dev)
+    if dx is not None:
+        _plain(dx, "dx", dt, shape, dev)
+    else:
+        dx = torch.empty_like(h) if hs == d else h.new_empty(shape)
+    ws, nb = None, 0
+    if with_dgain or with_dbias:
+        nb = _layer_norm_workspace(rows, d)
+        if nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    outs = []
+    for want, t, name in ((with_dgain, dgain, "dgain"), (with_dbias, dbias, "dbias")):
+        outs.append(None if not want else torch.empty(d, dtype=torch.float32, device=dev)
+                    if t is None else _plain(t, name, torch.float32, (d,), dev))
+    dgain, dbias = outs
+    st = f.sffn_layer_norm_backward(f.code[dt], f.code[gain.dtype], dy.data_ptr(), ys,
+                                    h.data_ptr(), hs, gain.data_ptr(), mean.data_ptr(),
+                                    rstd.data_ptr(), _ptr(dres), rs, rows, d, dx.data_ptr(),
+                                    _ptr(dgain), _ptr(dbias), _ptr(ws), nb, f.stream(dev.index))
+    if st:
+        _fail(st, "sffn_layer_norm_backward")
+    return dx, dgain, dbias
+
+
+@functools.lru_cache(maxsize=256)
+def _layer_norm_workspace(rows, d):
+    n = _SZ()
+    st = _lib().sffn_layer_norm_backward_workspace(rows, d, ctypes.byref(n))
+    if st:
+        _fail(st, "sffn_layer_norm_backward_workspace")
     return n.value
 
 

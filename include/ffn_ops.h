@@ -1,7 +1,8 @@
 /* ffn_ops.h -- C ABI of the operators around the sparse FFN layer of sparse_ffn.h, in the same
- * library (libsparse_ffn.so, MI355X / gfx950): the root-mean-square norm before the layer with
- * the residual stream's sum (also with an 8-bit output for serving), its gradient, products
- * with 4-bit weights for batches of few tokens, and the AdamW step over the layer's tensors.
+ * library (libsparse_ffn.so, MI355X / gfx950): the root-mean-square norm and the layer norm before
+ * the layer with the residual stream's sum (also with an 8-bit output for serving), their gradients,
+ * products with 4-bit weights for batches of few tokens and, with the tokens in 4 bits too, for
+ * prompts, the norm of all gradients and clipping by it, and the AdamW step over the layer's tensors.
  * All declarations here are interface of the library.
  *
  * Conventions are those of sparse_ffn.h: device pointers unless marked (host), row-major
@@ -11,12 +12,13 @@
  *     of a row are contiguous.  Pointers need only their element's alignment.
  *   - Zero rows (or elements, or tensors) are valid and launch nothing.
  *   - No output may overlap an input or another output (SFFN_ERR_INVALID_ARGUMENT), except where
- *     a call says that it updates in place, and the norm's h, and its y in dtype, which may be x
+ *     a call says that it updates in place, and a norm's h, and its y in dtype, which may be x
  *     or the residual itself (same address and stride).
  *   - Non-finite values follow the formulas: they reach the outputs that depend on them.
  *   - Results do not depend on timing: no call adds with atomics.
  *   - Kernel names for sffn_profile_read: rms_norm, rms_norm_fp8, rms_norm_grad,
- *     rms_norm_grad_sum, mx4_quantize, mx4_tile, mx4_linear, adamw. */
+ *     rms_norm_grad_sum, layer_norm, layer_norm_fp8, layer_norm_grad, layer_norm_grad_sum,
+ *     mx4_quantize, mx4_tile, mx4_linear, adamw. */
 #ifndef FFN_OPS_H_
 #define FFN_OPS_H_
 
@@ -77,6 +79,40 @@ sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const vo
                                      int64_t dres_stride, int64_t rows, int32_t d, void *dx,
                                      float *dgain, void *workspace, size_t workspace_bytes,
                                      void *stream);
+
+/* Layer norm of the residual stream, for `rows` tokens of length d:
+ *   h = x + residual  (h = x without one),  mean = mean(h),
+ *   rstd = 1 / sqrt(mean((h - mean)^2) + eps),  y = (h - mean) * rstd * gain + bias
+ * in fp32, from the unrounded h; the deviations are taken from the mean of the row's own values (no
+ * difference of two large sums), and their sum corrects that mean.  Types, strides and what may be
+ * NULL are as in sffn_rms_norm; gain and bias [d] have gain_dtype, bias may be NULL (0).
+ * mean and rstd [rows] fp32 may each be NULL. */
+sffn_status_t sffn_layer_norm(int32_t dtype, int32_t gain_dtype, const void *x, int64_t x_stride,
+                              const void *residual, int64_t residual_stride, const void *gain,
+                              const void *bias, float eps, int64_t rows, int32_t d, void *y,
+                              float *mean, float *rstd, void *h, void *stream);
+
+/* The same norm with its output in 8 bits and one scale a row, as sffn_rms_norm_fp8 gives it. */
+sffn_status_t sffn_layer_norm_fp8(int32_t dtype, int32_t gain_dtype, const void *x,
+                                  int64_t x_stride, const void *residual, int64_t residual_stride,
+                                  const void *gain, const void *bias, float eps, int64_t rows,
+                                  int32_t d, void *q, float *scale, void *h, void *stream);
+
+/* (host only) Bytes of scratch sffn_layer_norm_backward needs for these sizes with dgain or dbias: 0
+ * for few rows, which are summed without it. */
+sffn_status_t sffn_layer_norm_backward_workspace(int64_t rows, int32_t d, size_t *bytes);
+
+/* Gradient of sffn_layer_norm.  With xh = (h - mean) * rstd and t = dy * gain:
+ *   dx = rstd * (t - mean(t) - xh * mean(t * xh)) + dres,
+ *   dgain = sum over rows of dy * xh,   dbias = sum over rows of dy
+ * h, mean and rstd are the forward's.  dgain and dbias [d] are fp32 and may each be NULL; with zero
+ * rows they are cleared.  All else is as in sffn_rms_norm_backward. */
+sffn_status_t sffn_layer_norm_backward(int32_t dtype, int32_t gain_dtype, const void *dy,
+                                       int64_t dy_stride, const void *h, int64_t h_stride,
+                                       const void *gain, const float *mean, const float *rstd,
+                                       const void *dres, int64_t dres_stride, int64_t rows,
+                                       int32_t d, void *dx, float *dgain, float *dbias,
+                                       void *workspace, size_t workspace_bytes, void *stream);
 
 /* 4-bit weights.  Value of weight (n, k): e2m1(code) * 2^(s - 127), s = scales[n, k / 32] (255
  * is NaN), e2m1 codes 0..7 = 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 the sign (the OCP microscaling

@@ -1,0 +1,148 @@
+"""Host-only checks of the later operators of include/ffn_ops.h (layer norm, gradient norm and
+clipping, 4-bit tokens): bad arguments are refused before anything reaches the GPU.  Runs without
+a GPU."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+A = 0x1000  # stands for a device pointer; never followed
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+F32, BF16, E4M3 = 0, 1, 2
+B = 1 << 28  # distance of the stand-in arrays below: more than any of them is long
+
+
+@pytest.fixture(scope="module")
+def ops():
+    import activation_sparse_transformer_amd as sffn
+    from activation_sparse_transformer_amd import ffn_ops
+    if not os.path.exists(sffn.LIB_PATH):
+        pytest.fail("libsparse_ffn.so is not built (run __graft_entry__.build())")
+    return ffn_ops
+
+
+def _message():
+    from activation_sparse_transformer_amd import sparse_ffn
+    return sparse_ffn.last_error()
+
+
+NORM = dict(dtype=BF16, gain_dtype=BF16, x=A, x_stride=64, residual=A, residual_stride=64, gain=A, bias=A,
+            eps=1e-5, rows=0, d=64, y=A, mean=A, stat=A, h=A)
+
+
+def _norm(ops, a, fp8):
+    if fp8:
+        return ops._lib().sffn_layer_norm_fp8(*[v for k, v in a.items() if k != "mean"], None)
+    return ops._lib().sffn_layer_norm(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({}, OK), ({"dtype": 7}, INVALID), ({"dtype": E4M3}, INVALID), ({"gain_dtype": E4M3}, INVALID),
+    ({"dtype": F32, "gain_dtype": BF16}, INVALID), ({"gain_dtype": F32}, OK), ({"bias": None}, OK),
+    ({"d": 0}, INVALID), ({"d": -1}, INVALID), ({"d": 32769}, UNSUPPORTED), ({"rows": -1}, INVALID),
+    ({"rows": (1 << 40) + 1}, INVALID), ({"eps": -1e-6}, INVALID), ({"eps": float("nan")}, INVALID),
+    ({"residual": None}, INVALID), ({"rows": 2, "x": None}, INVALID), ({"rows": 2, "x_stride": 63}, INVALID),
+    ({"rows": 2, "residual_stride": 0}, INVALID), ({"rows": 2, "gain": None}, INVALID),
+    ({"rows": 2, "y": None}, INVALID), ({"rows": 2, "x": A + 1}, INVALID), ({"rows": 2, "h": A + 1}, INVALID),
+    ({"rows": 2, "stat": A + 2}, INVALID), ({"rows": 2, "gain": A + 1}, INVALID), ({"rows": 2, "bias": A + 1}, INVALID),
+])
+def test_norm_arguments(ops, kw, status):
+    for fp8 in (False, True):
+        assert _norm(ops, dict(NORM, **kw), fp8) == status
+
+
+def test_norm_statistics_arguments(ops):
+    assert _norm(ops, dict(NORM, rows=2, stat=None), True) == INVALID
+    assert _norm(ops, dict(NORM, rows=2, mean=A + 2), False) == INVALID
+
+
+AT = {k: (i + 1) * B for i, k in enumerate(("x", "residual", "gain", "bias", "y", "mean", "stat", "h"))}
+
+
+@pytest.mark.parametrize("out,over", [(o, i) for o in ("y", "mean", "stat", "h") for i in AT if i != o])
+def test_norm_overlap(ops, out, over):
+    """Outputs over inputs or one another, by their first and by their last bytes."""
+    size = {"x": 1280, "residual": 1280, "gain": 128, "bias": 128, "y": 1280, "mean": 40, "stat": 40, "h": 1280}
+    for fp8 in (False, True):
+        if fp8 and "mean" in (out, over):
+            continue
+        n = dict(size, y=640) if fp8 else size
+        for at in (AT[over] + n[over] - 4, AT[over] - n[out] + 4):
+            assert _norm(ops, dict(NORM, rows=10, **dict(AT, **{out: at})), fp8) == INVALID
+            assert "overlap" in _message()
+
+
+def test_norm_in_place_needs_the_same_rows(ops):
+    for kw in ({"x_stride": 80, "h": AT["x"]}, {"x_stride": 80, "y": AT["x"]}, {"residual_stride": 65, "h": AT["residual"]}):
+        assert _norm(ops, dict(NORM, rows=10, **dict(AT, **kw)), False) == INVALID and "overlap" in _message()
+    assert _norm(ops, dict(NORM, rows=10, **dict(AT, y=AT["x"])), True) == INVALID and "overlap" in _message()
+
+
+GRAD = dict(dtype=BF16, gain_dtype=F32, dy=A, dy_stride=64, h=A, h_stride=64, gain=A, mean=A, rstd=A, dres=A,
+            dres_stride=64, rows=20000, d=64, dx=A, dgain=A, dbias=A, ws=A, nb=1 << 30)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"rows": 0, "dgain": None, "dbias": None}, OK), ({"dtype": 5}, INVALID), ({"rows": -2}, INVALID),
+    ({"d": 40000}, UNSUPPORTED), ({"dy": None}, INVALID), ({"h": None}, INVALID), ({"h_stride": 32}, INVALID),
+    ({"dres_stride": 32}, INVALID), ({"rstd": None}, INVALID), ({"mean": None}, INVALID), ({"mean": A + 2}, INVALID),
+    ({"dx": None}, INVALID), ({"ws": None}, INVALID), ({"ws": A + 8}, INVALID), ({"nb": 16}, INVALID),
+    ({"dx": A + 1}, INVALID), ({"dgain": A + 1}, INVALID), ({"dbias": A + 2}, INVALID), ({"rows": 0}, INVALID),
+])
+def test_norm_backward_arguments(ops, kw, status):
+    assert ops._lib().sffn_layer_norm_backward(*dict(GRAD, **kw).values(), None) == status
+
+
+def test_norm_workspace(ops):
+    f, n = ops._lib(), ctypes.c_size_t()
+    for d in (1, 64, 2048, 16384, 16385, 32768):
+        for rows in (0, 1, 4, 1000, 1025, 100000, 1 << 30, 1 << 40):
+            assert f.sffn_layer_norm_backward_workspace(rows, d, ctypes.byref(n)) == OK
+            assert n.value % (d * 8) == 0 and n.value <= 512 * d * 8
+            if rows <= 1024 and (rows * d <= 1 << 20 or d > 16384):
+                assert n.value == 0  # few rows are summed in the same launch
+            elif d <= 16384 or rows > 1024:
+                assert n.value > 0
+    assert f.sffn_layer_norm_backward_workspace(4, 2048, None) == INVALID
+
+
+@pytest.mark.parametrize("rows,d", [(40, 64), (20000, 64), (3000, 20000)])
+def test_norm_backward_overlap(ops, rows, d):
+    ins, outs = ("dy", "h", "gain", "mean", "rstd", "dres"), ("dx", "dgain", "dbias")
+    far = 1 << 34
+    at = {k: (i + 1) * far for i, k in enumerate(ins + outs + ("ws",))}
+    base = dict(GRAD, rows=rows, d=d, dy_stride=d, h_stride=d, dres_stride=d)
+    for out in outs:
+        for over in ins + outs:
+            if out == over or (out, over) == ("dx", "dres"):
+                continue
+            a = dict(base, **dict(at, **{out: at[over]}))
+            assert ops._lib().sffn_layer_norm_backward(*a.values(), None) == INVALID, (out, over)
+            assert "overlap" in _message(), (out, over)
+    a = dict(base, **dict(at, dx=at["dres"], dres_stride=d + 2))
+    assert ops._lib().sffn_layer_norm_backward(*a.values(), None) == INVALID and "overlap" in _message()
+    n = ctypes.c_size_t()
+    ops._lib().sffn_layer_norm_backward_workspace(rows, d, ctypes.byref(n))
+    if n.value:
+        for over in ins + outs:
+            a = dict(base, **dict(at, ws=at[over]))
+            assert ops._lib().sffn_layer_norm_backward(*a.values(), None) == INVALID and "overlap" in _message(), over
+
+
+def test_binding_needs_device_tensors(ops):
+    import torch
+    x, g = torch.zeros(2, 64), torch.ones(64)
+    for call in (lambda: ops.layer_norm(x, g), lambda: ops.layer_norm_fp8(x, g),
+                 lambda: ops.layer_norm_backward(x, x, g, torch.ones(2), torch.ones(2))):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad"])
+def test_vector_accesses_are_declared_at_their_alignment(name):
+    """As for the earlier operators: a vector access to memory of an element's alignment is written as one."""
+    from activation_sparse_transformer_amd import build
+    r = subprocess.run([build.HIPCC, *build.FLAGS, "-Werror=align-mismatch", "-fsyntax-only", "--cuda-device-only",
+                        os.path.join(build.CSRC, name + ".hip")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
