@@ -155,6 +155,92 @@ sffn_status_t layer_norm(int32_t dtype, int32_t gain_dtype, const void* x, int64
   return api_run(fp8 ? "layer_norm_fp8" : "layer_norm", static_cast<hipStream_t>(stream), f);
 }
 
+// Elements of a workgroup of the gradient norm: all of them together are about GRAD_GROUPS, which keep
+// the memory busy and leave few partial sums.
+constexpr int64_t GRAD_GROUPS = 1024, GRAD_CHUNK_MIN = 4096;
+int64_t grad_chunk(const sffn_grad_t* grads, int32_t n_grads) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < n_grads; ++i) total += grads[i].n;
+  const int64_t units = (total + GRAD_GROUPS * GRAD_CHUNK_MIN - 1) / (GRAD_GROUPS * GRAD_CHUNK_MIN);
+  return (units > 1 ? units : 1) * GRAD_CHUNK_MIN;
+}
+int64_t grad_groups(const sffn_grad_t* grads, int32_t n_grads, int64_t chunk) {
+  int64_t groups = 0;
+  for (int32_t i = 0; i < n_grads; ++i) groups += (grads[i].n + chunk - 1) / chunk;
+  return groups;
+}
+
+sffn_status_t check_grad_sizes(const sffn_grad_t* grads, int32_t n_grads) {
+  if (n_grads < 0 || (n_grads > 0 && !grads)) return invalid("grads is NULL or its count negative");
+  int64_t total = 0;
+  for (int32_t i = 0; i < n_grads; ++i) {
+    if (grads[i].n < 0 || grads[i].n > (int64_t)1 << 40) return invalid("n of a gradient must be in [0, 2^40]");
+    total += grads[i].n;
+    if (total > (int64_t)1 << 50) return unsupported("all gradients must have at most 2^50 elements");
+  }
+  return SFFN_OK;
+}
+
+sffn_status_t grad_norm(const sffn_grad_t* grads, int32_t n_grads, double max_norm, float* norm,
+                        float* factor, void* workspace, size_t workspace_bytes, bool clip,
+                        void* stream) {
+  OPS_TRY(check_grad_sizes(grads, n_grads));
+  if (!(max_norm >= 0.0)) return invalid("max_norm must not be negative");
+  if (!norm) return invalid("norm is NULL");
+  if (misaligned(norm, 4) || misaligned(factor, 4)) return invalid("a pointer is not aligned to its element");
+  const Rows nr = block(norm, 4), fr = block(factor, 4), none = block(nullptr, 0);
+  OPS_TRY(check_overlap({nr, fr}, {none}));
+  for (int32_t i = 0; i < n_grads; ++i) {
+    const sffn_grad_t& g = grads[i];
+    if (g.dtype != SFFN_F32 && g.dtype != SFFN_BF16) return invalid("dtype must be SFFN_F32 or SFFN_BF16");
+    if (g.n == 0) continue;
+    if (!g.grad || (clip && !g.out)) return invalid("a gradient's pointer is NULL");
+    const size_t size = size_of(g.dtype);
+    if (misaligned(g.grad, size) || (clip && misaligned(g.out, size)))
+      return invalid("a pointer is not aligned to its element");
+  }
+  const int64_t chunk = grad_chunk(grads, n_grads), parts = grad_groups(grads, n_grads, chunk);
+  const size_t need = (size_t)parts * sizeof(double);
+  if (parts > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return invalid("workspace is NULL, misaligned or too small");
+  const Rows wr = block(parts > 0 ? workspace : nullptr, need);
+  OPS_TRY(check_overlap({nr, fr, wr}, {none}));
+  for (int32_t i = 0; i < n_grads; ++i) {
+    const uint64_t bytes = (uint64_t)grads[i].n * size_of(grads[i].dtype);
+    const Rows gr = block(grads[i].grad, bytes), outr = block(clip ? grads[i].out : nullptr, bytes);
+    OPS_TRY(check_overlap({nr, fr, wr, outr}, {outr.at == gr.at ? none : gr}));
+    OPS_TRY(check_overlap({nr, fr, wr}, {gr}));
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  GradTable tab;
+  std::memset(&tab, 0, sizeof(tab));
+  tab.chunk = chunk;
+  tab.part = static_cast<double*>(workspace);
+  int used = 0;
+  int64_t groups = 0;
+  auto flush = [&]() -> sffn_status_t {
+    if (used == 0) return SFFN_OK;
+    for (int i = used; i < GRAD_TENSORS; ++i) tab.first[i] = 0xffffffffu;
+    auto f = [&] { return launch_grad_norm(tab, (uint32_t)groups, s); };
+    const sffn_status_t st = api_run("grad_norm", s, f);
+    tab.part += groups;
+    used = 0;
+    groups = 0;
+    return st;
+  };
+  for (int32_t i = 0; i < n_grads; ++i) {
+    if (grads[i].n == 0) continue;
+    if (used == GRAD_TENSORS) OPS_TRY(flush());
+    tab.grad[used] = grads[i].grad;
+    tab.n[used] = grads[i].dtype == SFFN_BF16 ? -grads[i].n : grads[i].n;
+    tab.first[used++] = (uint32_t)groups;
+    groups += (grads[i].n + chunk - 1) / chunk;
+  }
+  OPS_TRY(flush());
+  auto f = [&] { return launch_grad_norm_sum(static_cast<double*>(workspace), parts, max_norm, norm, factor, s); };
+  return api_run("grad_norm_sum", s, f);
+}
+
 sffn_status_t check_mx4(int32_t N, int32_t K) {
   if (N < 0) return invalid("N must not be negative");
   if (K < 1) return invalid("K must be positive");
@@ -372,6 +458,57 @@ sffn_status_t sffn_mx4_linear(const void* tiled, int32_t N, int32_t K, int32_t x
                   y_dtype == SFFN_BF16, y};
   auto f = [&] { return launch_mx4_linear(a, static_cast<hipStream_t>(stream)); };
   return api_run("mx4_linear", static_cast<hipStream_t>(stream), f);
+}
+
+sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t* grads, int32_t n_grads, size_t* bytes) {
+  OPS_TRY(check_grad_sizes(grads, n_grads));
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = (size_t)grad_groups(grads, n_grads, grad_chunk(grads, n_grads)) * sizeof(double);
+  return SFFN_OK;
+}
+
+sffn_status_t sffn_grad_norm(const sffn_grad_t* grads, int32_t n_grads, double max_norm, float* norm,
+                             float* factor, void* workspace, size_t workspace_bytes, void* stream) {
+  return grad_norm(grads, n_grads, max_norm, norm, factor, workspace, workspace_bytes, false, stream);
+}
+
+sffn_status_t sffn_grad_clip(const sffn_grad_t* grads, int32_t n_grads, double max_norm, float* norm,
+                             float* factor, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!factor) return invalid("factor is NULL");
+  OPS_TRY(grad_norm(grads, n_grads, max_norm, norm, factor, workspace, workspace_bytes, true, stream));
+  ScaleTable tab;
+  std::memset(&tab, 0, sizeof(tab));
+  tab.factor = factor;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  // a launch stays below 2^32 threads; a longer tensor is cut into parts of whole chunks
+  constexpr int64_t MAX_GROUPS = ((int64_t)1 << 31) / 256;
+  int used = 0;
+  int64_t groups = 0;
+  auto flush = [&]() -> sffn_status_t {
+    if (used == 0) return SFFN_OK;
+    for (int i = used; i < SCALE_TENSORS; ++i) tab.first[i] = 0xffffffffu;
+    auto f = [&] { return launch_grad_scale(tab, (uint32_t)groups, s); };
+    const sffn_status_t st = api_run("grad_scale", s, f);
+    used = 0;
+    groups = 0;
+    return st;
+  };
+  for (int32_t i = 0; i < n_grads; ++i) {
+    const size_t size = size_of(grads[i].dtype);
+    int64_t at = 0;
+    while (at < grads[i].n) {
+      if (used == SCALE_TENSORS || groups == MAX_GROUPS) OPS_TRY(flush());
+      const int64_t room = (MAX_GROUPS - groups) * SCALE_CHUNK;
+      const int64_t n = grads[i].n - at < room ? grads[i].n - at : room;
+      tab.grad[used] = static_cast<const char*>(grads[i].grad) + at * (int64_t)size;
+      tab.out[used] = static_cast<char*>(grads[i].out) + at * (int64_t)size;
+      tab.n[used] = grads[i].dtype == SFFN_BF16 ? -n : n;
+      tab.first[used++] = (uint32_t)groups;
+      groups += (n + SCALE_CHUNK - 1) / SCALE_CHUNK;
+      at += n;
+    }
+  }
+  return flush();
 }
 
 sffn_status_t sffn_adamw_step(const sffn_adamw_tensor_t* tensors, int32_t n_tensors,

@@ -399,6 +399,33 @@ struct Mx4Args {
 };
 hipError_t launch_mx4_linear(const Mx4Args& a, hipStream_t s);
 
+// Gradients of one launch of the norm or of the scaling; the table travels as kernel arguments.
+// n is negated for bf16.
+constexpr int GRAD_TENSORS = 128;
+struct GradTable {
+  const void* grad[GRAD_TENSORS];
+  int64_t n[GRAD_TENSORS];
+  uint32_t first[GRAD_TENSORS];  // first workgroup of each tensor; 2^32 - 1 past the last one
+  int64_t chunk;                 // elements of a workgroup, a multiple of 8
+  double* part;                  // [workgroups] sums of squares
+};
+static_assert(sizeof(GradTable) <= 4096 - 256, "kernel arguments");
+hipError_t launch_grad_norm(const GradTable& t, uint32_t groups, hipStream_t s);
+// norm and factor (may be null) of the n partial sums
+hipError_t launch_grad_norm_sum(const double* part, int64_t n, double max_norm, float* norm,
+                                float* factor, hipStream_t s);
+constexpr int SCALE_TENSORS = 96;
+constexpr int SCALE_CHUNK = 8192;  // elements of one workgroup
+struct ScaleTable {
+  const void* grad[SCALE_TENSORS];
+  void* out[SCALE_TENSORS];
+  int64_t n[SCALE_TENSORS];  // negated for bf16
+  uint32_t first[SCALE_TENSORS];
+  const float* factor;
+};
+static_assert(sizeof(ScaleTable) <= 4096 - 256, "kernel arguments");
+hipError_t launch_grad_scale(const ScaleTable& t, uint32_t groups, hipStream_t s);
+
 // Tensors of one AdamW launch; the table travels as kernel arguments (at most 4 KB of them).
 constexpr int ADAMW_TENSORS = 48;
 struct AdamwTable {

@@ -43,11 +43,16 @@ class AdamwHyperC(ctypes.Structure):
                [("step", _I64)]
 
 
+class GradC(ctypes.Structure):
+    _fields_ = [("grad", _P), ("out", _P), ("n", _I64), ("dtype", _I32), ("zero", _I32)]
+
+
 _GRAD_WORD = AdamwTensorC.grad.offset // 8
 _SHAPE, _DTYPE = attrgetter("shape"), attrgetter("dtype")
 
 _NORM = [_I32, _I32, _P, _I64, _P, _I64, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _P]
 _LAYER_NORM = _NORM[:7] + [_P] + _NORM[7:]
+_GRAD_NORM = [_P, _I32, ctypes.c_double, _P, _P, _P, _SZ, _P]
 _PROTOS = {
     "sffn_rms_norm": _NORM,
     "sffn_rms_norm_fp8": _NORM,
@@ -63,6 +68,9 @@ _PROTOS = {
     "sffn_mx4_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
     "sffn_mx4_tile": [_P, _P, _I32, _I32, _P, _P],
     "sffn_mx4_linear": [_P, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _I32, _P, _P],
+    "sffn_grad_norm_workspace": [_P, _I32, ctypes.POINTER(_SZ)],
+    "sffn_grad_norm": _GRAD_NORM,
+    "sffn_grad_clip": _GRAD_NORM,
     "sffn_adamw_step": [ctypes.POINTER(AdamwTensorC), _I32, _I32, _I32, _I32,
                         ctypes.POINTER(AdamwHyperC), _P, _P],
 }
@@ -531,6 +539,87 @@ class Mx4Linear:
         if st:
             _fail(st, "sffn_mx4_linear")
         return y
+
+
+def _spans(tensors):
+    return sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                  for t in tensors if t.numel())
+
+
+def _grads(grads, max_norm, out, clip, norm, factor, stream):
+    f = _lib()
+    torch = f.torch
+    T = torch.Tensor
+    if not grads:
+        raise ValueError("no gradients")
+    dev = grads[0].device
+    if _elsewhere(f, dev, stream):
+        with _on(dev, stream, norm, factor, *grads, *(out or ())):
+            return _grads(grads, max_norm, out, clip, norm, factor, None)
+    n = len(grads)
+    types = list(map(_DTYPE, grads))
+    if not set(types) <= {torch.float32, torch.bfloat16} or set(map(T.get_device, grads)) != {dev.index} \
+            or not all(map(T.is_contiguous, grads)):
+        raise ValueError(f"gradients must be contiguous float32 or bfloat16 tensors on {dev}")
+    ptrs = list(map(T.data_ptr, grads))
+    words = np.zeros((n, 4), dtype=np.int64)
+    words[:, 0] = ptrs
+    words[:, 2] = list(map(T.numel, grads))
+    words[:, 3] = [f.code[t] for t in types]
+    if clip:
+        if out is not None:
+            if len(out) != n or list(map(_DTYPE, out)) != types \
+                    or list(map(_SHAPE, out)) != list(map(_SHAPE, grads)) \
+                    or set(map(T.get_device, out)) != {dev.index} or not all(map(T.is_contiguous, out)):
+                raise ValueError("out must have a contiguous tensor of each gradient's shape and "
+                                 f"type, on {dev}")
+            # nothing is written over what has yet to be read or written, but a gradient by itself
+            moved = [(g, o) for g, o in zip(grads, out) if g.data_ptr() != o.data_ptr()]
+            spans = _spans([*grads, *(o for _, o in moved)]) if moved else _spans(grads)
+        else:
+            out, spans = grads, _spans(grads)
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("two of the tensors overlap")
+        words[:, 1] = list(map(T.data_ptr, out))
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    else:
+        _plain(norm, "norm", torch.float32, (1,), dev)
+    if factor is not None:
+        _plain(factor, "factor", torch.float32, (1,), dev)
+    elif max_norm is not None:
+        factor = torch.empty(1, dtype=torch.float32, device=dev)
+    table = words.ctypes.data
+    nb = _SZ()
+    st = f.sffn_grad_norm_workspace(table, n, ctypes.byref(nb))
+    if st:
+        _fail(st, "sffn_grad_norm_workspace")
+    ws = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    fn = f.sffn_grad_clip if clip else f.sffn_grad_norm
+    st = fn(table, n, 0.0 if max_norm is None else max_norm, norm.data_ptr(), _ptr(factor),
+            ws.data_ptr(), nb.value, f.stream(dev.index))
+    if st:
+        _fail(st, "sffn_grad_clip" if clip else "sffn_grad_norm")
+    return norm, factor
+
+
+def grad_norm(grads, max_norm=None, norm=None, factor=None, stream=None):
+    """The norm of all gradients (a list of contiguous device tensors, each float32 or bfloat16)
+    together, and with max_norm the factor that clips them to it: 1, or max_norm / norm above it.
+    Returns (norm, factor), float32 [1] on the device (factor None without max_norm): factor is
+    what AdamW.step takes as grad_scale, with no pass over the gradients of its own.  Sums are in
+    64 bits.  An infinity among the gradients gives the norm infinity and the factor 0, a NaN
+    gives NaN.  norm and factor may be given."""
+    if factor is not None and max_norm is None:
+        raise ValueError("factor needs max_norm")
+    return _grads(grads, max_norm, None, False, norm, factor, stream)
+
+
+def clip_grads(grads, max_norm, out=None, norm=None, factor=None, stream=None):
+    """The same, and the gradients times the factor: in place, or into `out` (a list of tensors
+    like grads, each of which may be its gradient itself).  The tensors written and read may not
+    overlap otherwise.  Returns (norm, factor)."""
+    return _grads(grads, max_norm, out, True, norm, factor, stream)
 
 
 class AdamW:

@@ -18,7 +18,7 @@
  *   - Results do not depend on timing: no call adds with atomics.
  *   - Kernel names for sffn_profile_read: rms_norm, rms_norm_fp8, rms_norm_grad,
  *     rms_norm_grad_sum, layer_norm, layer_norm_fp8, layer_norm_grad, layer_norm_grad_sum,
- *     mx4_quantize, mx4_tile, mx4_linear, adamw. */
+ *     mx4_quantize, mx4_tile, mx4_linear, grad_norm, grad_norm_sum, grad_scale, adamw. */
 #ifndef FFN_OPS_H_
 #define FFN_OPS_H_
 
@@ -149,6 +149,40 @@ sffn_status_t sffn_mx4_linear(const void *tiled, int32_t N, int32_t K, int32_t x
                               const void *x, int64_t x_stride, const float *x_scale, int32_t T,
                               const float *bias, int32_t relu, int32_t y_dtype, void *y,
                               void *stream);
+
+/* One gradient: n elements of its own type (SFFN_F32 or SFFN_BF16). */
+typedef struct {
+  const void *grad;
+  void *out;       /* sffn_grad_clip: where it goes, grad itself to clip in place */
+  int64_t n;
+  int32_t dtype;
+  int32_t zero;    /* 0 */
+} sffn_grad_t;
+
+/* (host only) Bytes of scratch sffn_grad_norm and sffn_grad_clip need for these gradients (host
+ * array, of which only n is read). */
+sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t *grads, int32_t n_grads, size_t *bytes);
+
+/* Norm of all gradients together (host array, read before the call returns; out is not read):
+ *   norm[0] = sqrt(sum of the squares of all elements),
+ *   factor[0] = 1 if norm <= max_norm, else max_norm / norm
+ * with the squares, exact in 64 bits, summed in 64 bits, so that no square overflows or vanishes;
+ * norm is rounded to fp32 once, and so is the quotient, by that norm.  factor is what
+ * sffn_adamw_step takes as grad_scale; it may be NULL.  An infinity among the gradients gives the
+ * norm infinity and, with a finite max_norm, the factor 0; a NaN gives NaN for both.  No gradients, or none with elements,
+ * have the norm 0.  The order of the sums depends on the sizes alone.  workspace: as many bytes as
+ * sffn_grad_norm_workspace says, 16-byte aligned. */
+sffn_status_t sffn_grad_norm(const sffn_grad_t *grads, int32_t n_grads, double max_norm,
+                             float *norm, float *factor, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* The same, and then out = grad * factor (rounded once to the gradient's type) for every gradient.
+ * Where out is grad itself and factor is 1, nothing is written.  factor is required.  An out may be
+ * its own gradient, and may overlap nothing else of its own call; the outs of different gradients,
+ * and an out and another gradient, are the caller's to keep apart. */
+sffn_status_t sffn_grad_clip(const sffn_grad_t *grads, int32_t n_grads, double max_norm,
+                             float *norm, float *factor, void *workspace, size_t workspace_bytes,
+                             void *stream);
 
 /* One tensor of an AdamW step (device pointers, n elements each). */
 typedef struct {

@@ -130,16 +130,71 @@ def test_norm_backward_overlap(ops, rows, d):
             assert ops._lib().sffn_layer_norm_backward(*a.values(), None) == INVALID and "overlap" in _message(), over
 
 
+GRADIENT = dict(grad=1 * B, out=2 * B, n=300, dtype=F32, zero=0)
+CALL = dict(max_norm=1.0, norm=5 * B, factor=6 * B, ws=7 * B, nb=1 << 20)
+
+
+def _grad_call(ops, name, tensors, kw):
+    arr = (ops.GradC * max(1, len(tensors)))(*[ops.GradC(**dict(GRADIENT, **t)) for t in tensors])
+    a = dict(CALL, **kw)
+    return getattr(ops._lib(), name)(ctypes.byref(arr), len(tensors), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,call,status", [
+    ({"n": -1}, {}, INVALID), ({"n": (1 << 40) + 1}, {}, INVALID), ({"dtype": E4M3}, {}, INVALID),
+    ({"grad": None}, {}, INVALID), ({"grad": A + 2}, {}, INVALID), ({"dtype": BF16, "grad": A + 1}, {}, INVALID),
+    ({}, {"max_norm": -1.0}, INVALID), ({}, {"max_norm": float("nan")}, INVALID), ({}, {"norm": None}, INVALID),
+    ({}, {"norm": A + 2}, INVALID), ({}, {"factor": A + 2}, INVALID), ({}, {"ws": None}, INVALID),
+    ({}, {"ws": 7 * B + 8}, INVALID), ({}, {"nb": 7}, INVALID),
+])
+def test_grad_norm_arguments(ops, kw, call, status):
+    for name in ("sffn_grad_norm", "sffn_grad_clip"):
+        assert _grad_call(ops, name, [kw], call) == status, name
+
+
+def test_grad_clip_arguments(ops):
+    for kw, call in (({"out": None}, {}), ({"out": 2 * B + 2}, {}), ({}, {"factor": None})):
+        assert _grad_call(ops, "sffn_grad_clip", [kw], call) == INVALID
+    f, n = ops._lib(), ctypes.c_size_t()
+    assert f.sffn_grad_norm(None, 1, 1.0, A, A, A, 8, None) == INVALID
+    assert f.sffn_grad_norm(None, -1, 1.0, A, A, A, 8, None) == INVALID
+    assert f.sffn_grad_norm_workspace(None, 0, ctypes.byref(n)) == OK and n.value == 0
+    assert f.sffn_grad_norm_workspace(None, 0, None) == INVALID
+
+
+def test_grad_norm_workspace(ops):
+    """About 1024 parts, and one more for each tensor's end."""
+    f, n = ops._lib(), ctypes.c_size_t()
+    for sizes in ([1], [4096], [4097], [0, 5, 0], [1 << 22], [(1 << 22) + 1] * 3, [1 << 40] * 4, [77] * 500):
+        arr = (ops.GradC * len(sizes))(*[ops.GradC(n=k) for k in sizes])
+        assert f.sffn_grad_norm_workspace(ctypes.byref(arr), len(sizes), ctypes.byref(n)) == OK
+        assert n.value % 8 == 0 and sum(k > 0 for k in sizes) <= n.value // 8 <= 1024 + len(sizes)
+    many = (ops.GradC * 1100)(*[ops.GradC(n=1 << 40) for _ in range(1100)])
+    assert f.sffn_grad_norm_workspace(ctypes.byref(many), 1100, ctypes.byref(n)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,call", [
+    ({}, {"norm": 6 * B}), ({}, {"norm": 1 * B + 1196}), ({}, {"factor": 1 * B}), ({}, {"ws": 1 * B + 1184}),
+    ({}, {"ws": 5 * B}), ({}, {"norm": 2 * B}), ({}, {"factor": 2 * B + 1196}), ({}, {"ws": 2 * B}),
+    ({"out": 1 * B + 4}, {}), ({"out": 1 * B - 1196}, {}),
+])
+def test_grad_clip_overlap(ops, kw, call):
+    assert _grad_call(ops, "sffn_grad_clip", [kw], call) == INVALID and "overlap" in _message()
+    if not kw and 2 * B not in call.values() and 2 * B + 1196 not in call.values():
+        assert _grad_call(ops, "sffn_grad_norm", [kw], call) == INVALID and "overlap" in _message()
+
+
 def test_binding_needs_device_tensors(ops):
     import torch
     x, g = torch.zeros(2, 64), torch.ones(64)
     for call in (lambda: ops.layer_norm(x, g), lambda: ops.layer_norm_fp8(x, g),
-                 lambda: ops.layer_norm_backward(x, x, g, torch.ones(2), torch.ones(2))):
+                 lambda: ops.layer_norm_backward(x, x, g, torch.ones(2), torch.ones(2)),
+                 lambda: ops.grad_norm([x]), lambda: ops.clip_grads([x], 1.0)):
         with pytest.raises(ValueError):
             call()
 
 
-@pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad"])
+@pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad", "k_grad_norm"])
 def test_vector_accesses_are_declared_at_their_alignment(name):
     """As for the earlier operators: a vector access to memory of an element's alignment is written as one."""
     from activation_sparse_transformer_amd import build
