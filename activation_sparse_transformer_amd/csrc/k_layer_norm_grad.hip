@@ -10,28 +10,32 @@
 // order (no atomics: the result depends on the sizes alone).  Where registers do not hold the
 // column sums (above 16384 columns), or where the second launch would take longer than reading a
 // few rows twice, further workgroups of the first launch sum the columns from dy and h themselves.
+// Bound by memory: 16384 x 2304 bf16 with dres moves 302 MB in 57 us (5.3 TB/s, both launches; 62 without
+// the next row's loads in flight), 8192 x 4096 268 MB in 45.  Above 8192 columns a lane has two vectors
+// and no registers for the next row (2048 x 16384: 58 us, 4.7 TB/s; fp32 spills some), above 16384
+// dy and h are read twice (1024 x 32768: 134 us).
 #include "ops_common.hpp"
 
 namespace sffn {
 namespace {
 
-constexpr int grad_threads(int L) { return L < 256 ? 256 : L; }
-
-// Column sums of grad_columns(B) columns over the rows of one of a.sum_parts parts, by the B threads of a
-// workgroup: 64 row groups of lanes of 4 columns, joined in order.
-constexpr int grad_columns(int B) { return B / 16; }
-template <typename T, int B>
+// Column sums of GRAD_COLUMNS columns over the rows of one of a.sum_parts parts, by a workgroup of any
+// number of waves: every 4 lanes take a row, 4 columns each; the 16 rows of a wave are joined by lane
+// rotations, the waves in LDS, in order.
+constexpr int GRAD_COLUMNS = 16;
+template <typename T>
 __device__ __forceinline__ void sum_columns(const LayerNormGradArgs& a, int blk) {
-  constexpr int GROUPS = 64, LANES = B / GROUPS, COLUMNS = grad_columns(B);
-  __shared__ float join[2][GROUPS][COLUMNS + 1];
-  const int blocks = (a.d + COLUMNS - 1) / COLUMNS, part = blk / blocks, col0 = blk % blocks * COLUMNS;
-  const int c4 = (int)(threadIdx.x % LANES) * 4, g = (int)(threadIdx.x / LANES);
+  __shared__ float join[2][16][GRAD_COLUMNS];
+  const int groups = (int)blockDim.x / 4, waves = (int)blockDim.x / 64;
+  const int blocks = (a.d + GRAD_COLUMNS - 1) / GRAD_COLUMNS;
+  const int part = blk / blocks, col0 = blk % blocks * GRAD_COLUMNS;
+  const int c4 = (int)(threadIdx.x & 3) * 4, g = (int)(threadIdx.x >> 2);
   const int col = col0 + c4, n = a.d - col;
   const int64_t per = (a.rows + a.sum_parts - 1) / a.sum_parts, first = part * per;
   const int64_t last = first + per < a.rows ? first + per : a.rows;
-  float sg[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+  float s[2][4] = {};
 #pragma unroll 4
-  for (int64_t row = first + g; row < last; row += GROUPS) {
+  for (int64_t row = first + g; row < last; row += groups) {
     const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride + col;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride + col;
     const float rstd = a.rstd[row], mean = a.mean[row];
@@ -40,120 +44,163 @@ __device__ __forceinline__ void sum_columns(const LayerNormGradArgs& a, int blk)
     load4<false>(h, n, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sg[i] += y[i] * ((x[i] - mean) * rstd);
-      sb[i] += y[i];
+      s[0][i] += y[i] * ((x[i] - mean) * rstd);
+      s[1][i] += y[i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    join[0][g][c4 + i] = sg[i];
-    join[1][g][c4 + i] = sb[i];
-  }
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v = s[k][i];
+      v += dpp<0x128>(v);  // rotations of a row's 16 lanes by 8 and by 4
+      v += dpp<0x124>(v);
+      v = rows_reduce(v, Add());
+      if ((threadIdx.x & 63) < 4) join[k][threadIdx.x >> 6][c4 + i] = v;
+    }
   __syncthreads();
-  const int c = (int)threadIdx.x % COLUMNS, which = (int)threadIdx.x / COLUMNS;
+  const int c = (int)threadIdx.x % GRAD_COLUMNS, which = (int)threadIdx.x / GRAD_COLUMNS;
   if (which < 2 && col0 + c < a.d) {
-    float t = 0.f;
-#pragma unroll 16
-    for (int i = 0; i < GROUPS; ++i) t += join[which][i][c];
+    float t = join[which][0][c];
+    for (int i = 1; i < waves; ++i) t += join[which][i][c];
     float* out = a.part ? a.part + ((int64_t)part * 2 + which) * a.d : which == 0 ? a.dgain : a.dbias;
     if (out) out[col0 + c] = t;
   }
 }
 
-// B threads: B / L rows at a time, by row_groups workgroups; the ones past them sum columns.
-// SUMS: the row groups sum the columns in registers, into a.part if it is given.
-template <typename T, typename G, int NV, int L, int B, bool SUMS>
-__global__ __launch_bounds__(B) void layer_norm_grad_kernel(LayerNormGradArgs a, int row_groups) {
+// A workgroup takes blockDim / lanes rows at a time, L lanes each, or with L = 0 row_waves waves;
+// row_groups workgroups take the rows in turn, the ones past them sum columns.  SUMS: the row groups
+// sum the columns in registers, into a.part if it is given.  With one vector a lane, a row is loaded
+// while the one before it is reduced and written.
+template <typename T, typename G, int NV, int L, bool SUMS>
+__global__ __launch_bounds__(1024) void layer_norm_grad_kernel(LayerNormGradArgs a, int row_groups,
+                                                               int row_waves) {
   if constexpr (!SUMS) {
     if ((int)blockIdx.x >= row_groups) {
-      sum_columns<T, B>(a, (int)blockIdx.x - row_groups);
+      sum_columns<T>(a, (int)blockIdx.x - row_groups);
       return;
     }
   }
-  constexpr int RPB = B / L;
-  __shared__ float red[4][L > 64 ? L / 64 : 1];
-  __shared__ float join[SUMS && RPB > 1 ? RPB * 8 * L : 1];
-  const int li = (int)(threadIdx.x % L), grp = (int)(threadIdx.x / L);
+  constexpr bool AHEAD = SUMS && NV == 1, ONE = L == 1024;
+  __shared__ float red[4][16];
+  __shared__ float join[SUMS && !ONE ? 8 * 1024 : 1];
+  const int lanes = L > 0 ? L : 64 * row_waves;
+  const int grp = ONE ? 0 : L > 0 ? (int)threadIdx.x / L : uniform((int)threadIdx.x / lanes);
+  const int li = (int)threadIdx.x - grp * lanes, rpb = ONE ? 1 : (int)blockDim.x / lanes;
   const int d = a.d;
   const bool tail = (d & 7) != 0;
   const G* gain = static_cast<const G*>(a.gain);
   const float inv_d = 1.f / (float)d;
 
+  // gains of more than two vectors a lane are loaded where they are needed
+  constexpr bool HELD = NV <= 2;
   Raw8<G> rg[NV];
-  float ag[SUMS ? NV : 1][8], ab[SUMS ? NV : 1][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = (v * L + li) * 8;
+  const auto load_gain = [&](int v) {
+    const int e = (v * lanes + li) * 8;
     rg[v].zero();
     if (e + 8 <= d) rg[v].load(gain + e);
     else if (e < d) rg[v].load_n(gain + e, d - e);
+  };
+  float ag[SUMS ? NV : 1][8], ab[SUMS ? NV : 1][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (HELD) load_gain(v);
     if constexpr (SUMS) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ag[v][i] = ab[v][i] = 0.f;
     }
   }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows;
-       row += (int64_t)row_groups * RPB, turn ^= 2) {
+  Raw8<T> ry[NV], rh[NV], rr[NV];
+  float rstd = 0.f, mean = 0.f;
+  const auto load = [&](int64_t row) {  // past the last row: nothing, which adds nothing
+    const bool have = ONE || row < a.rows;
     const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
     const T* dres = static_cast<const T*>(a.dres) + row * a.dres_stride;
-    const float rstd = a.rstd[row], mean = a.mean[row];
-    Raw8<T> ry[NV], rh[NV], rr[NV];
+    if (!ONE) rstd = mean = 0.f;
+    if (have) {
+      rstd = a.rstd[row];
+      mean = a.mean[row];
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = (v * L + li) * 8;
+      const int e = (v * lanes + li) * 8;
       ry[v].zero();
       rh[v].zero();
-      if (e + 8 <= d) {
+      if (have && e + 8 <= d) {
         ry[v].load(dy + e);
         rh[v].load(h + e);
       }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = (v * L + li) * 8;
+      const int e = (v * lanes + li) * 8;
       rr[v].zero();
-      if (a.dres && e + 8 <= d) rr[v].load(dres + e);
+      if (a.dres && have && e + 8 <= d) rr[v].load(dres + e);
     }
     if (tail) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int e = (v * L + li) * 8;
-        if (e < d && e + 8 > d) {
+        const int e = (v * lanes + li) * 8;
+        if (have && e < d && e + 8 > d) {
           ry[v].load_n(dy + e, d - e);
           rh[v].load_n(h + e, d - e);
           if (a.dres) rr[v].load_n(dres + e, d - e);
         }
       }
     }
+  };
+  const int64_t step = (int64_t)row_groups * rpb;
+  int turn = 0;
+  if constexpr (AHEAD) load((int64_t)blockIdx.x * rpb + grp);
+  for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += step, turn ^= 2) {
+    const int64_t row = row0 + grp;
+    if constexpr (!AHEAD) load(row);
+    // what the output needs of this row, when the next one's loads take the place of its own
+    float t[AHEAD ? 8 : 1], xh[AHEAD ? 8 : 1], res[AHEAD ? 8 : 1];
+    const float rs = rstd;
     float st = 0.f, sx = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int n = d - (v * L + li) * 8;  // past the row's end a deviation is 0, not -mean
+      const int n = d - (v * lanes + li) * 8;  // past the row's end a deviation is 0, not -mean
+      if constexpr (!HELD) load_gain(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float c = n >= 8 || (tail && i < n) ? rh[v].get(i) - mean : 0.f;
-        const float y = ry[v].get(i), p = y * (c * rstd), g = rg[v].get(i);
+        const float c = n >= 8 || (tail && i < n) ? (rh[v].get(i) - mean) * rs : 0.f;
+        const float y = ry[v].get(i), p = y * c, g = rg[v].get(i);
         if constexpr (SUMS) {
           ag[v][i] += p;
           ab[v][i] += y;
         }
         st += y * g;
         sx += p * g;
+        if constexpr (AHEAD) {
+          t[i] = y * g;
+          xh[i] = c;
+          res[i] = rr[v].get(i);
+        }
       }
     }
-    row_reduce2<L>(st, sx, red[turn], red[turn + 1]);
+    if constexpr (AHEAD) load(row + step);
+    if constexpr (L == 0 || L == 1024) {
+      group_sum2(st, sx, red[turn], red[turn + 1], L == 0 ? row_waves : 16, L == 0 ? grp * row_waves : 0);
+    } else {
+      st = lane_reduce<L>(st, Add());
+      sx = lane_reduce<L>(sx, Add());
+    }
+    if (!ONE && row >= a.rows) continue;  // (of the last turn; the barrier is behind)
     const float ct = st * inv_d, cx = sx * inv_d;
     T* dx = static_cast<T*>(a.dx) + row * d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = (v * L + li) * 8;
+      const int e = (v * lanes + li) * 8;
+      if constexpr (!HELD) load_gain(v);
       float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        o[i] = rstd * (ry[v].get(i) * rg[v].get(i) - ct - (rh[v].get(i) - mean) * rstd * cx) +
-               rr[v].get(i);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (AHEAD) o[i] = rs * (t[i] - ct - xh[i] * cx) + res[i];
+        else o[i] = rs * (ry[v].get(i) * rg[v].get(i) - ct - (rh[v].get(i) - mean) * rs * cx) + rr[v].get(i);
+      }
       if (e + 8 <= d) store8(dx + e, o);
       else if (e < d) store8_n(dx + e, o, d - e);
     }
@@ -163,24 +210,23 @@ __global__ __launch_bounds__(B) void layer_norm_grad_kernel(LayerNormGradArgs a,
     float* part = a.part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if constexpr (RPB > 1) {
+      if (!ONE && rpb > 1) {
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           __syncthreads();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            join[grp * 8 * L + i * L + li] = which == 0 ? ag[v][i] : ab[v][i];
+            join[(grp * 8 + i) * lanes + li] = which == 0 ? ag[v][i] : ab[v][i];
           __syncthreads();
-          for (int c = (int)threadIdx.x; c < 8 * L; c += B) {
+          for (int c = (int)threadIdx.x; c < 8 * lanes; c += (int)blockDim.x) {
             float s = 0.f;
-#pragma unroll
-            for (int g = 0; g < RPB; ++g) s += join[g * 8 * L + c];
-            const int col = (v * L + c % L) * 8 + c / L;
+            for (int g = 0; g < rpb; ++g) s += join[g * 8 * lanes + c];
+            const int col = (v * lanes + c % lanes) * 8 + c / lanes;
             if (col < d) part[which * d + col] = s;
           }
         }
       } else {
-        const int e = (v * L + li) * 8;
+        const int e = (v * lanes + li) * 8;
         if (e + 8 <= d) {
           store8(part + e, ag[v]);
           store8(part + d + e, ab[v]);
@@ -218,40 +264,56 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* 
 
 // Where the row groups sum the columns in registers: not above 16384 columns (they would spill), and
 // not for few rows, for which reading dy and h once more is less than a second launch.
-bool sums_in_rows(int64_t rows, int32_t d) {
-  return d <= 16384 && !(rows <= 1024 && rows * d <= 1 << 20);
+bool few_rows(int64_t rows, int32_t d) { return rows <= 1024 && rows * d <= 1 << 20; }
+bool sums_in_rows(int64_t rows, int32_t d) { return d <= 16384 && !few_rows(rows, d); }
+// Rows of a workgroup: as few as make 8 waves.  (With 256 workgroups, 16384 x 2304 bf16 in 2 x 5 waves
+// takes 56.4 us, in 5 69, in 3 x 5 57.4; 8192 x 4096 in 8 44.9, in 16 49.1.)
+struct GradShape {
+  RowShape row;
+  int rows;
+  int threads() const { return rows * (row.lanes > 0 ? row.lanes : 64 * row.waves); }
+};
+GradShape grad_shape(int32_t d) {
+  const RowShape r = row_shape(d, false);
+  if (r.nv > 1) return {{1024, 16, r.nv}, 1};  // (registers: a fixed number of lanes takes fewer)
+  return {r, r.lanes > 0 ? 512 / r.lanes : (8 + r.waves - 1) / r.waves};
 }
-// Workgroups of the rows: each one's partial rows cost a write and a read, so there are only as many
-// as keep the memory busy, with equal numbers of rows.
+// Workgroups of the rows: one for a CU, with equal numbers of rows.  More would write and read more
+// partial rows (16384 x 2304: 512 take 63.4 us, 384 unequally spread over the CUs 77).
 int row_groups(int64_t rows, int32_t d) {
-  const int L = norm_lanes(d, true), rpb = grad_threads(L) / L;
+  const int rpb = grad_shape(d).rows;
   const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = sums_in_rows(rows, d) ? (L > 512 ? 256 : 512) : 1 << 20;
+  const int64_t most = sums_in_rows(rows, d) ? 256 : 1 << 20;
   const int64_t turns = (need + most - 1) / most;
   return (int)((need + turns - 1) / turns);
 }
 // Parts of the rows whose columns other workgroups sum: one where that needs no second launch.
 int sum_parts(int64_t rows, int32_t d) {
-  if (rows <= 1024 && rows * d <= 1 << 20) return 1;
+  if (few_rows(rows, d)) return 1;
   const int64_t parts = (rows + 1023) / 1024;
   return (int)(parts < 64 ? parts : 64);
 }
 
 template <typename T, typename G>
 hipError_t launch_t(const LayerNormGradArgs& a0, hipStream_t s) {
-  return norm_shape<true>(a0.d, [&](auto lanes, auto nv) {
-    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value, B = grad_threads(L);
+  const GradShape shape = grad_shape(a0.d);
+  return with_row_shape<1024>(shape.row, [&](auto lanes, auto nv) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
     LayerNormGradArgs a = a0;
     const int groups = row_groups(a.rows, a.d);
-    if constexpr (NV * L <= 2048) {
+    const dim3 threads((unsigned)shape.threads());
+    if constexpr (NV <= 2) {
       if (sums_in_rows(a.rows, a.d)) {
-        layer_norm_grad_kernel<T, G, NV, L, B, true><<<dim3((unsigned)groups), dim3(B), 0, s>>>(a, groups);
+        layer_norm_grad_kernel<T, G, NV, L, true>
+            <<<dim3((unsigned)groups), threads, 0, s>>>(a, groups, shape.row.waves);
         return hipGetLastError();
       }
     }
     a.sum_parts = sum_parts(a.rows, a.d);
-    const int sums = a.dgain || a.dbias ? a.sum_parts * ((a.d + grad_columns(B) - 1) / grad_columns(B)) : 0;
-    layer_norm_grad_kernel<T, G, NV, L, B, false><<<dim3((unsigned)(groups + sums)), dim3(B), 0, s>>>(a, groups);
+    const int blocks = (a.d + GRAD_COLUMNS - 1) / GRAD_COLUMNS;
+    const int sums = a.dgain || a.dbias ? a.sum_parts * blocks : 0;
+    layer_norm_grad_kernel<T, G, NV, L, false>
+        <<<dim3((unsigned)(groups + sums)), threads, 0, s>>>(a, groups, shape.row.waves);
     return hipGetLastError();
   });
 }

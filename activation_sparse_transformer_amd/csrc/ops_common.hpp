@@ -164,13 +164,10 @@ __device__ __forceinline__ float max_abs(float a, float v) {
   return __uint_as_float(x > y ? x : y);
 }
 // Reduction over 16 lanes, a half wave (32) or a wave (64); every lane gets the result.
-// quad_perm, half-row and row mirrors combine the 16 lanes of a row, the lane swaps the rows.
-template <int LANES, typename Op>
-__device__ __forceinline__ float lane_reduce(float v, Op op) {
-  v = op(v, dpp<0xB1>(v));   // quad_perm [1, 0, 3, 2]
-  v = op(v, dpp<0x4E>(v));   // quad_perm [2, 3, 0, 1]
-  v = op(v, dpp<0x141>(v));  // half-row mirror
-  v = op(v, dpp<0x140>(v));  // row mirror
+// quad_perm, half-row and row mirrors combine the 16 lanes of a row, the lane swaps the rows
+// (rows_reduce: those alone).
+template <int LANES = 64, typename Op>
+__device__ __forceinline__ float rows_reduce(float v, Op op) {
   if constexpr (LANES >= 32) {
     const uint32_t u = __float_as_uint(v);
     const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
@@ -182,6 +179,14 @@ __device__ __forceinline__ float lane_reduce(float v, Op op) {
     v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
   }
   return v;
+}
+template <int LANES, typename Op>
+__device__ __forceinline__ float lane_reduce(float v, Op op) {
+  v = op(v, dpp<0xB1>(v));   // quad_perm [1, 0, 3, 2]
+  v = op(v, dpp<0x4E>(v));   // quad_perm [2, 3, 0, 1]
+  v = op(v, dpp<0x141>(v));  // half-row mirror
+  v = op(v, dpp<0x140>(v));  // row mirror
+  return rows_reduce<LANES>(v, op);
 }
 // The same over the L lanes of a row (16, 32, 64, or whole waves of one workgroup); `red` holds
 // L / 64 floats of LDS that nothing else uses before the next barrier.
@@ -197,25 +202,34 @@ __device__ __forceinline__ float row_reduce(float v, Op op, float* red) {
   }
   return v;
 }
-// Sums of two values over the L lanes of a row, with one barrier.
-template <int L>
-__device__ __forceinline__ void row_reduce2(float& a, float& b, float* red_a, float* red_b) {
-  a = lane_reduce<(L < 64 ? L : 64)>(a, Add());
-  b = lane_reduce<(L < 64 ? L : 64)>(b, Add());
-  if constexpr (L > 64) {
-    if ((threadIdx.x & 63) == 0) {
-      red_a[threadIdx.x >> 6] = a;
-      red_b[threadIdx.x >> 6] = b;
-    }
+// A row's reduction for any number of waves: L lanes (16, 32, 64), or with L = 0 all waves of the
+// workgroup (at most 16), whose values 16 lanes of each wave take up again.  `red` holds 16 floats
+// of LDS that nothing else uses before the next barrier; 0 is op's neutral element.
+template <int L, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op, float* red) {
+  v = lane_reduce<(L == 0 ? 64 : L)>(v, op);
+  if constexpr (L == 0) {
+    const int i = (int)(threadIdx.x & 15);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    a = red_a[0];
-    b = red_b[0];
-#pragma unroll
-    for (int i = 1; i < L / 64; ++i) {
-      a += red_a[i];
-      b += red_b[i];
-    }
+    v = lane_reduce<16>(i < (int)(blockDim.x >> 6) ? red[i] : 0.f, op);
   }
+  return v;
+}
+// Sums of two values over `waves` waves, of which `first` is the first, with one barrier of the
+// workgroup.
+__device__ __forceinline__ void group_sum2(float& a, float& b, float* red_a, float* red_b,
+                                           int waves, int first) {
+  a = lane_reduce<64>(a, Add());
+  b = lane_reduce<64>(b, Add());
+  const int i = (int)(threadIdx.x & 15);
+  if ((threadIdx.x & 63) == 0) {
+    red_a[threadIdx.x >> 6] = a;
+    red_b[threadIdx.x >> 6] = b;
+  }
+  __syncthreads();
+  a = lane_reduce<16>(i < waves ? red_a[first + i] : 0.f, Add());
+  b = lane_reduce<16>(i < waves ? red_b[first + i] : 0.f, Add());
 }
 // Quotients of values up to 448 s by a positive scale s, bit for bit the divide's: the product with
 // the rounded reciprocal is a few roundings off, and one fma with its remainder corrects it
@@ -321,6 +335,39 @@ hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a,
 // dgain[c] = sum of the n partial rows (0 with none)
 hipError_t launch_rms_norm_grad_sum(const float* part, int n, int32_t d, float* dgain,
                                     hipStream_t s);
+
+// How a layer norm's kernels share a row of d elements: L lanes (16, 32, 64; several rows a
+// workgroup), or L = 0: `waves` whole waves, as many as the row's vectors of 8 need at nv a lane.
+struct RowShape {
+  int lanes, waves, nv;
+};
+constexpr int rows_of(int lanes) { return lanes == 0 ? 1 : 256 / (lanes + (lanes == 0)); }  // of 4 waves
+// wide: 16 elements a lane also where 8 would do (bf16 rows of the forward: 16384 x 2304 takes 51.8 us
+// and 45.9 with 8 bits out, 54.9 and 54.9 with 8; fp32 rows, with as many bytes in 8, lose 2%).
+inline RowShape row_shape(int32_t d, bool wide) {
+  if (d <= 128) return {16, 4, 1};
+  if (d <= 256) return {32, 4, 1};
+  if (d <= 512) return {64, 4, 1};
+  const int units = (d + 511) / 512;
+  int nv = (units + 15) / 16;
+  if (wide && nv < 2) nv = 2;
+  return {0, (units + nv - 1) / nv, nv};
+}
+// Calls f(lanes, vectors) with both as integral constants; MANY: the lanes of more than one vector.
+template <int MANY, typename F>
+hipError_t with_row_shape(const RowShape& r, F&& f) {
+#define SFFN_SHAPE(l, n) \
+  if (r.lanes == l && r.nv == n) return f(std::integral_constant<int, l>(), std::integral_constant<int, n>())
+  SFFN_SHAPE(16, 1);
+  SFFN_SHAPE(32, 1);
+  SFFN_SHAPE(64, 1);
+  SFFN_SHAPE(0, 1);
+  SFFN_SHAPE(MANY, 2);
+  SFFN_SHAPE(MANY, 3);
+  SFFN_SHAPE(MANY, 4);
+#undef SFFN_SHAPE
+  return hipErrorInvalidValue;
+}
 
 struct LayerNormArgs {
   const void* x;
