@@ -16,5 +16,5 @@ from .sparse_ffn import (  # noqa: F401
 )
 from .ffn_ops import (  # noqa: F401
     rms_norm, rms_norm_fp8, rms_norm_backward, layer_norm, layer_norm_fp8, layer_norm_backward,
-    mx4_quantize, Mx4Linear, grad_norm, clip_grads, AdamW,
+    mx4_quantize, Mx4Linear, Mx4Tokens, grad_norm, clip_grads, AdamW,
 )

@@ -1,0 +1,443 @@
+// Products of 4-bit tokens with 4-bit weights: y = act(x W^T + bias).
+//
+// The scaled matrix instructions multiply e2m1 values whose groups of 32 columns have their own powers
+// of two; a product of two of them has at most 4 bits, and their sum comes out within two fp32 roundings
+// (exact where the scales of a row differ by up to 2^4).  A lane of an operand holds 32 columns of a row in
+// 16 bytes, and their scale in a byte.
+//
+// Both operands come in blocks of 16 rows x 128 columns (MX4_BLOCK bytes): units of 16 bytes, lane by
+// lane, lane (q, r) = 16 q + r being the one of row r.  In a block of tokens, unit (q, r) is columns 32 q to
+// 32 q + 31, as the instructions take them.  A block of weights is in the order of the few-token product
+// of bf16 values: word g of unit (q, r) is columns 32 g + 8 q to 32 g + 8 q + 7, so what the instructions
+// want is the transpose over q and the words; swaps of lane rows give it.
+#include <utility>
+
+#include "ops_common.hpp"
+
+namespace sffn {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// s_waitcnt for at most n vector-memory operations in flight, and for all LDS operations.
+constexpr int vmcnt(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int LGKM0 = 0xC07F;
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, int sa, u32x4 b, int sb, f32x4 c) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, sa, 0, sb);
+}
+
+// Direct loads to LDS, 16 bytes a lane, lane after lane: of 1 KB at base + at (both uniform: a buffer load,
+// which needs no address arithmetic in vector registers), and of each lane's own 16 bytes.
+__device__ __forceinline__ void load_block(const uint8_t* base, uint32_t at, int lane, u32x4* lds) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, -1, 0x00027000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)lds, 16, lane * 16, at, 0, 0);
+}
+__device__ __forceinline__ void load_units(const uint8_t* from, u32x4* lds) {
+  __builtin_amdgcn_global_load_lds(from, (lds_ptr)lds, 16, 0, 0);
+}
+
+// Orders a wave's accesses to its own piece of LDS: the hardware carries them out in order, only
+// the compiler has to keep it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ float finish(float v, float bias, bool relu) {
+  v += bias;
+  return relu && v < 0.f ? 0.f : v;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
+}
+// Four bias values from n on, 0 past the last one.
+__device__ __forceinline__ f32x4 bias4(const float* bias, int n, int N) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (!bias) return v;
+  if (n + 4 <= N) return *reinterpret_cast<const f32x4_a4*>(bias + n);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < N) v[e] = bias[n + e];
+  return v;
+}
+
+// ------------------------------------------------------------------ many tokens
+// 32 x 32 x 64 products (6.1 to 6.6 PFLOP/s from registers alone, where 16 x 16 x 128 ones reach 4.3 to
+// 5.4).  WN x WT waves, each with NP pairs of blocks of weight rows by TP pairs of blocks of tokens.  The
+// operands of 128 columns are a stage of LDS, filled by direct loads two stages ahead.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int WN, int WT, int NP, int TP>
+struct Form {
+  static constexpr int WAVES = WN * WT;
+  static constexpr int NW = WN * NP * 2, TW = WT * TP * 2;  // blocks of a workgroup
+  static constexpr int BLOCKS = NW + TW;
+  static constexpr int LOADS = BLOCKS / WAVES;  // of codes, of a wave and stage; and one of scales
+  static constexpr int SCALE_LOADS = (BLOCKS + 15) / 16;
+  static constexpr int UNITS = BLOCKS * 64 + SCALE_LOADS * 64;  // 16-byte units of a stage
+  // where a wave turns its results: two waves' places in a stage's memory
+  static constexpr int F32_PAIRS = NP >= 2 && 2 * 32 * 17 <= UNITS ? 2 : 1;
+  static constexpr int REGION = 32 * ((F32_PAIRS * 8 > NP * 4 ? F32_PAIRS * 8 : NP * 4) + 1);
+  static_assert(WAVES == 4 && 2 * REGION <= UNITS, "results in LDS");
+  // workgroups of a CU, by LDS and by the registers of the sums and fragments
+  static constexpr int REGS = NP * TP * 16 + NP * 18 + TP * 18 + 20;
+  static constexpr int BY_LDS = 160 * 1024 / (3 * UNITS * 16), BY_REGS = 512 / REGS * 4 / WAVES;
+  static constexpr int PER_CU = BY_LDS < BY_REGS ? BY_LDS : BY_REGS;
+  static_assert(BLOCKS % WAVES == 0 && SCALE_LOADS <= WAVES && PER_CU >= 1, "loads of a stage");
+};
+
+template <int OP>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, int sa, u32x4 b, int sb, f32x16 c) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, OP, sa, OP, sb);
+}
+
+// The results of a wave, NP x TP products, from token tok0 and row n0 on; PAIRS: pairs of blocks of rows at a
+// time.  Element e of a product, lane (h, row): weight row 8 (e / 4) + 4 h + e % 4, token `row`.
+template <typename Y, int NP, int TP, int PAIRS>
+__device__ __forceinline__ void write_tile(const Mx4MatmulArgs& a, const f32x16 (&acc)[NP][TP], u32x4* own,
+                                           int64_t tok0, int n0, int lane) {
+  constexpr int PER = 16 / (int)sizeof(Y);              // elements of a unit
+  constexpr int ROW = PAIRS * 32 / PER, PITCH = ROW + 1;  // units of a token
+  const int h = lane >> 5, row = lane & 31, N = a.d.N;
+  const float floor = a.relu ? 0.f : -INFINITY;
+#pragma unroll
+  for (int g = 0; g < NP; g += PAIRS) {
+    f32x4 bias[PAIRS][4];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bias[i][j] = bias4(a.bias, n0 + (g + i) * 32 + 8 * j + 4 * h, N);
+#pragma unroll
+    for (int t = 0; t < TP; ++t) {
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = acc[g + i][t][4 * j + e] + bias[i][j][e];
+            v[e] = v[e] < floor ? floor : v[e];
+          }
+          Y* to = reinterpret_cast<Y*>(own + row * PITCH) + i * 32 + 8 * j + 4 * h;
+          if constexpr (sizeof(Y) == 2)
+            *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+          else
+            *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
+        }
+      wave_fence();
+      constexpr int TOKENS = 64 / ROW;  // of an access
+#pragma unroll
+      for (int k = 0; k < 32 / TOKENS; ++k) {
+        const int r = k * TOKENS + lane / ROW, u = lane % ROW;
+        const u32x4 o = own[r * PITCH + u];
+        const int64_t tok = tok0 + t * 32 + r;
+        const int n = n0 + g * 32 + u * PER;
+        if (tok >= a.T) continue;
+        Y* y = static_cast<Y*>(a.y) + tok * N + n;
+        if (n + PER <= N) {
+          store_v<false>(y, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (n + e < N) y[e] = sizeof(Y) == 2 ? (Y)(o[e >> 1] >> (16 * (e & 1))) : __uint_as_float(o[e & 3]);
+        }
+      }
+    }
+  }
+}
+
+template <int WN, int WT, int NP, int TP>
+__global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void mx4_matmul_kernel(
+    Mx4MatmulArgs a) {
+  typedef Form<WN, WT, NP, TP> F;
+  __shared__ u32x4 s0[F::UNITS], s1[F::UNITS], s2[F::UNITS];
+  const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
+  const int h = lane >> 5, row = lane & 31;  // lane (h, row) of a 32-row operand
+  const int wn = wave % WN, wt = wave / WN;
+  const int nb = a.d.nb, kbs = a.d.kb, tb = (a.T + 15) / 16;
+
+  // The tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD takes consecutive tiles,
+  // and those run over 8 tiles of tokens first, so that what its workgroups read at a time fits its L2.
+  const int tn = (nb + F::NW - 1) / F::NW, tt = (tb + F::TW - 1) / F::TW, total = tn * tt;
+  const int xcd = (int)blockIdx.x & 7, lin = (int)blockIdx.x / 8 + xcd * (total / 8) + (xcd < total % 8 ? xcd : total % 8);
+  const int group = lin / (8 * tn), gt = tt - group * 8 < 8 ? tt - group * 8 : 8, rem = lin - group * 8 * tn;
+  const int n0 = rem / gt * F::NW, t0 = (group * 8 + rem % gt) * F::TW;
+
+  // Sources of this wave's direct loads, as buffers (the lane's and the stage's offsets need no address
+  // arithmetic); blocks past the last one are read as the last one.
+  const auto block_at = [&](int b) {
+    const bool w = b < F::NW;
+    int i = w ? n0 + b : t0 + b - F::NW;
+    const int last = (w ? nb : tb) - 1;
+    i = i < last ? i : last;
+    return static_cast<const uint8_t*>(w ? a.tiled : a.tokens) + (size_t)i * kbs * MX4_BLOCK;
+  };
+  const uint8_t* src[F::LOADS];
+#pragma unroll
+  for (int i = 0; i < F::LOADS; ++i) src[i] = block_at(wave * F::LOADS + i);
+  const int sl = wave % F::SCALE_LOADS;  // (several waves may load the same scales to the same place)
+  const int sb = sl * 16 + (lane >> 2);
+  const uint8_t* scale_src = block_at(sb < F::BLOCKS ? sb : F::BLOCKS - 1) + 1024 + (lane & 3) * 16;
+
+  const auto issue = [&](int kb, u32x4* s) __attribute__((always_inline)) {
+    const uint32_t at = (uint32_t)kb * MX4_BLOCK;
+#pragma unroll
+    for (int i = 0; i < F::LOADS; ++i)
+      load_block(src[i], at, lane, s + (wave * F::LOADS + i) * 64);
+    load_units(scale_src + at, s + F::BLOCKS * 64 + sl * 64);
+  };
+
+  // Fragments of a stage.  A row has four scales in a word; the lanes of h = 1 take the odd groups.
+  const int unit = (row >> 4) * 64 + (row & 15);  // of lane row in a pair of blocks, q = 0
+  const int w_at = wn * NP * 128 + unit + 32 * h, x_at = (F::NW + wt * TP * 2) * 64 + unit + 16 * h;
+  const int ws_at = wn * NP * 32 + row, xs_at = (F::NW + wt * TP * 2) * 16 + row;
+  u32x4 w[2][NP][2], x[2][TP][2];
+  uint32_t ws[2][NP], xs[2][TP];
+  const auto fragments = [&](const u32x4* s, int c) __attribute__((always_inline)) {
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(s + F::BLOCKS * 64);
+#pragma unroll
+    for (int t = 0; t < TP; ++t) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) x[c][t][k] = s[x_at + t * 128 + k * 32];
+      xs[c][t] = sc[xs_at + t * 32];
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      w[c][i][0] = s[w_at + i * 128];
+      w[c][i][1] = s[w_at + i * 128 + 16];
+      ws[c][i] = sc[ws_at + i * 32];
+    }
+  };
+  f32x16 acc[NP][TP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int t = 0; t < TP; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][t][e] = 0.f;
+
+  // A stage, whose fragments are in registers (set c).  Once every wave has them its buffer is free for the
+  // stage three ahead; the next stage is in when only the one after it may still be loading, and its
+  // fragments are read while this one's products run.  Past the end the last stage is loaded again, into
+  // buffers that nothing reads.
+  const auto stage = [&](int kb, u32x4* s, const u32x4* next, int c) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(vmcnt(F::LOADS + 1));
+    __builtin_amdgcn_s_waitcnt(LGKM0);
+    __asm__ volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(kb + 3 < kbs ? kb + 3 : kbs - 1, s);
+    fragments(next, c ^ 1);
+    u32x4 wt4[NP][2];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const u32x4 u = w[c][i][0], v = w[c][i][1];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // groups 2 k (h = 0) and 2 k + 1 (h = 1)
+        const auto p = __builtin_amdgcn_permlane32_swap(u[2 * k], u[2 * k + 1], false, false);
+        const auto r = __builtin_amdgcn_permlane32_swap(v[2 * k], v[2 * k + 1], false, false);
+        wt4[i][k] = u32x4{p[0], r[0], p[1], r[1]};
+      }
+      ws[c][i] >>= 8 * h;
+    }
+#pragma unroll
+    for (int t = 0; t < TP; ++t) xs[c][t] >>= 8 * h;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<0>(wt4[i][0], (int)ws[c][i], x[c][t][0], (int)xs[c][t], acc[i][t]);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<2>(wt4[i][1], (int)ws[c][i], x[c][t][1], (int)xs[c][t], acc[i][t]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  issue(0, s0);
+  issue(1 < kbs ? 1 : 0, s1);
+  issue(2 < kbs ? 2 : kbs - 1, s2);
+  __builtin_amdgcn_s_waitcnt(vmcnt(2 * (F::LOADS + 1)));
+  __asm__ volatile("s_barrier" ::: "memory");
+  fragments(s0, 0);
+  for (int kb = 0;;) {
+    stage(kb, s0, s1, 0);
+    if (++kb == kbs) break;
+    stage(kb, s1, s2, 1);
+    if (++kb == kbs) break;
+    stage(kb, s2, s0, 0);
+    if (++kb == kbs) break;
+    stage(kb, s0, s1, 1);
+    if (++kb == kbs) break;
+    stage(kb, s1, s2, 0);
+    if (++kb == kbs) break;
+    stage(kb, s2, s0, 1);
+    if (++kb == kbs) break;
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt(0));  // the repeated loads land before LDS goes away
+
+  // The results go through LDS, a wave's 32 tokens by 64 to 128 rows at a time, so that whole cache lines
+  // are written: pieces of 32 bytes a token, as a wave holds them, took three times as long.
+  __asm__ volatile("s_barrier" ::: "memory");  // the fragments of every wave are read
+  u32x4* own = (wave < 2 ? s0 : s1) + (wave & 1) * F::REGION;
+  const int64_t tok0 = (int64_t)(t0 + wt * TP * 2) * 16;
+  const int n = (n0 + wn * NP * 2) * 16;
+  if (a.y_bf16) write_tile<uint16_t, NP, TP, NP>(a, acc, own, tok0, n, lane);
+  else write_tile<float, NP, TP, F::F32_PAIRS>(a, acc, own, tok0, n, lane);
+}
+
+// ------------------------------------------------------------------ few tokens
+// Eight waves split the columns (KS) or take further rows; every wave loads its weights and tokens as the
+// instruction takes them (weights: swapped lane rows), and the waves' sums are added in order.
+constexpr int FEW_WAVES = 8;
+
+// The transpose over a lane's words and the four lane rows.
+__device__ __forceinline__ u32x4 transpose(u32x4 w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+template <int TT, int RB, int KS>
+__global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4MatmulArgs a) {
+  constexpr int PART = RB * TT * 64;
+  __shared__ f32x4 part[FEW_WAVES * PART];
+  const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
+  const int q = lane >> 4, r = lane & 15, kbs = a.d.kb, tb = (a.T + 15) / 16;
+  const int wg0 = (int)blockIdx.x * (RB * FEW_WAVES / KS), rb0 = wg0 + wave / KS * RB;
+  const int tb0 = (int)blockIdx.y * TT;
+  const uint8_t *w[RB], *x[TT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int i = rb0 + b < a.d.nb ? rb0 + b : a.d.nb - 1;
+    w[b] = static_cast<const uint8_t*>(a.tiled) + (size_t)i * kbs * MX4_BLOCK;
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int i = tb0 + t < tb ? tb0 + t : tb - 1;
+    x[t] = static_cast<const uint8_t*>(a.tokens) + (size_t)i * kbs * MX4_BLOCK;
+  }
+  f32x4 acc[RB][TT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int kb = wave % KS; kb < kbs; kb += KS) {
+    const size_t at = (size_t)kb * MX4_BLOCK;
+    u32x4 wc[RB], xc[TT];
+    int ws[RB], xs[TT];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      wc[b] = *reinterpret_cast<const u32x4*>(w[b] + at + lane * 16);
+      ws[b] = w[b][at + 1024 + r * 4 + q];
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      xc[t] = *reinterpret_cast<const u32x4*>(x[t] + at + lane * 16);
+      xs[t] = x[t][at + 1024 + r * 4 + q];
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const u32x4 wt = transpose(wc[b]);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[b][t] = mfma(wt, ws[b], xc[t], xs[t], acc[b][t]);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[wave * PART + (b * TT + t) * 64 + lane] = acc[b][t];
+  __syncthreads();
+  const int N = a.d.N;
+  for (int i = (int)threadIdx.x; i < FEW_WAVES / KS * PART; i += FEW_WAVES * 64) {
+    const int g = i / PART, at = i % PART, l = at & 63, t = (at >> 6) % TT, b = (at >> 6) / TT;
+    f32x4 s = part[g * KS * PART + at];
+#pragma unroll
+    for (int v = 1; v < KS; ++v) s += part[(g * KS + v) * PART + at];
+    const int64_t tok = (int64_t)(tb0 + t) * 16 + (l & 15);
+    const int n = (wg0 + g * RB + b) * 16 + (l >> 4) * 4;
+    if (tok >= a.T || n >= N) continue;
+    const f32x4 bias = bias4(a.bias, n, N);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = finish(s[e], bias[e], a.relu);
+    if (a.y_bf16) {
+      uint16_t* y = static_cast<uint16_t*>(a.y) + tok * N + n;
+      if (n + 4 <= N) {
+        *reinterpret_cast<u32x2_a2*>(y) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      } else {
+        for (int e = 0; e < N - n; ++e) y[e] = f32_to_bf16(v[e]);
+      }
+    } else {
+      float* y = static_cast<float*>(a.y) + tok * N + n;
+      if (n + 4 <= N) {
+        *reinterpret_cast<f32x4_a4*>(y) = f32x4{v[0], v[1], v[2], v[3]};
+      } else {
+        for (int e = 0; e < N - n; ++e) y[e] = v[e];
+      }
+    }
+  }
+}
+
+template <int WN, int WT, int NP, int TP>
+hipError_t launch_form(const Mx4MatmulArgs& a, hipStream_t s) {
+  typedef Form<WN, WT, NP, TP> F;
+  const int64_t tn = (a.d.nb + F::NW - 1) / F::NW, tt = ((a.T + 15) / 16 + F::TW - 1) / F::TW;
+  mx4_matmul_kernel<WN, WT, NP, TP><<<dim3((unsigned)(tn * tt)), F::WAVES * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int TT, int RB, int KS>
+hipError_t launch_few(const Mx4MatmulArgs& a, hipStream_t s) {
+  constexpr int ROWS = RB * FEW_WAVES / KS;
+  const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)(((a.T + 15) / 16 + TT - 1) / TT));
+  mx4_matmul_few_kernel<TT, RB, KS><<<grid, FEW_WAVES * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
+  const char* e = getenv("SFFN_FORM");
+  const int f = e ? atoi(e) : 0;
+  if (f == 0) {
+    if (a.T <= 16) return launch_few<1, 1, 8>(a, s);
+    if (a.T <= 32) return launch_few<2, 1, 8>(a, s);
+    if (a.T <= 64) return launch_few<4, 1, 8>(a, s);
+    const int64_t tiles = (int64_t)((a.d.nb + 15) / 16) * ((a.T + 255) / 256);
+    if (tiles < 256) return launch_form<2, 2, 2, 2>(a, s);
+    return launch_form<2, 2, 4, 2>(a, s);
+  }
+  switch (f) {
+    case 1: return launch_form<2, 2, 4, 2>(a, s);
+    case 2: return launch_form<2, 2, 2, 4>(a, s);
+    case 3: return launch_form<2, 2, 2, 2>(a, s);
+    case 4: return launch_form<2, 2, 1, 1>(a, s);
+    case 5: return launch_form<2, 2, 2, 1>(a, s);
+    case 6: return launch_form<2, 2, 4, 4>(a, s);
+    case 7: return launch_form<4, 1, 2, 2>(a, s);
+    case 8: return launch_few<4, 1, 8>(a, s);
+    case 9: return launch_few<4, 2, 8>(a, s);
+    case 10: return launch_few<4, 2, 4>(a, s);
+    case 11: return launch_few<1, 1, 8>(a, s);
+    case 12: return launch_few<1, 2, 8>(a, s);
+    case 13: return launch_few<1, 2, 4>(a, s);
+    case 14: return launch_few<1, 4, 4>(a, s);
+    case 15: return launch_few<1, 4, 8>(a, s);
+    case 16: return launch_few<1, 4, 2>(a, s);
+    case 17: return launch_few<2, 2, 8>(a, s);
+    case 18: return launch_few<2, 2, 4>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace sffn

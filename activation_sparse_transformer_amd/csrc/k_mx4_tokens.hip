@@ -1,0 +1,85 @@
+// Rounding of tokens to 4 bits (the format of the weights: e2m1 codes, one power of two per 32 columns),
+// in the layout that the products of mx4_matmul read.
+//
+// A lane takes 8 consecutive values, so that a wave reads 512 columns of a row in one piece; the four
+// lanes of a group find its absolute maximum and convert (the instruction rounds to nearest-even and
+// saturates; compared with the thresholds on 4 million values at every scale).  A workgroup collects 16
+// rows of four blocks of 128 columns in LDS, whose codes and scales it writes in one piece each.
+#include "ops_common.hpp"
+
+namespace sffn {
+namespace {
+
+constexpr int SPAN = 4;  // blocks of 128 columns of a workgroup
+
+template <typename T>
+__global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t stride, int32_t rows,
+                                                         int32_t K, int32_t kb, uint8_t* tokens) {
+  __shared__ uint32_t codes[SPAN * 256];
+  __shared__ uint8_t scales[SPAN * 64];
+  const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
+  const int kb0 = (int)blockIdx.x * SPAN;
+  const int64_t t0 = (int64_t)blockIdx.y * 16;
+  const int64_t k0 = (int64_t)kb0 * 128 + lane * 8;
+  const int n = K - k0 >= 8 ? 8 : K > k0 ? (int)(K - k0) : 0;
+  Raw8<T> raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + i * 4 + wave;
+    raw[i].zero();
+    if (t < rows) {
+      const T* p = x + t * stride + k0;
+      if (n == 8) raw[i].load(p);
+      else if (n > 0) raw[i].load_n(p, n);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 4 + wave;
+    float big = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) big = max_abs(big, raw[i].get(j));
+    big = max_abs(big, dpp<0xB1>(big));
+    big = max_abs(big, dpp<0x4E>(big));
+    // exponent of the largest value less 2 (e2m1's largest); infinity or NaN: scale 255, codes 0
+    const uint32_t bits = __float_as_uint(big);
+    const bool bad = bits >= 0x7f800000u;
+    const int e = (int)(bits >> 23) - 2;
+    const uint32_t scale = bad ? 255u : (uint32_t)(e < 0 ? 0 : e);
+    const float s = __uint_as_float(scale << 23);  // the exponent field alone counts
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(0), raw[i].get(1), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(2), raw[i].get(3), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(4), raw[i].get(5), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(6), raw[i].get(7), s, 3);
+    const int b = lane >> 4, q = (lane >> 2) & 3;
+    codes[b * 256 + (q * 16 + r) * 4 + (lane & 3)] = bad ? 0u : c;
+    // a group past the last column has the scale 1, as in the weights
+    if ((lane & 3) == 0) scales[b * 64 + r * 4 + q] = (uint8_t)(k0 < K ? scale : 127u);
+  }
+  __syncthreads();
+  const int b = (int)(threadIdx.x >> 6);
+  uint8_t* out = tokens + ((int64_t)blockIdx.y * kb + kb0) * MX4_BLOCK;
+  if (kb0 + b < kb)
+    *reinterpret_cast<u32x4*>(out + b * MX4_BLOCK + lane * 16) =
+        reinterpret_cast<const u32x4*>(codes)[threadIdx.x];
+  if (threadIdx.x < SPAN * 16 && kb0 + (int)(threadIdx.x >> 4) < kb)
+    *reinterpret_cast<uint32_t*>(out + (threadIdx.x >> 4) * MX4_BLOCK + 1024 + (threadIdx.x & 15) * 4) =
+        reinterpret_cast<const uint32_t*>(scales)[threadIdx.x];
+}
+
+}  // namespace
+
+hipError_t launch_mx4_tokens(bool bf16, const void* x, int64_t stride, int32_t T, int32_t K,
+                             void* tokens, hipStream_t s) {
+  const int kb = (int)(((int64_t)K + 127) / 128);
+  const dim3 grid((unsigned)((kb + SPAN - 1) / SPAN), (unsigned)((T + 15) / 16));
+  uint8_t* out = static_cast<uint8_t*>(tokens);
+  if (bf16)
+    mx4_tokens_kernel<uint16_t><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(x), stride, T, K, kb, out);
+  else
+    mx4_tokens_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(x), stride, T, K, kb, out);
+  return hipGetLastError();
+}
+
+}  // namespace sffn

@@ -251,6 +251,17 @@ sffn_status_t check_mx4(int32_t N, int32_t K) {
   return SFFN_OK;
 }
 
+// Tokens in 4 bits are blocks as the weights are.
+sffn_status_t check_tokens(int32_t T, int32_t K) {
+  if (T < 0) return invalid("T must not be negative");
+  if (K < 1) return invalid("K must be positive");
+  if (T > 1 << 20) return unsupported("T must be at most 2^20");  // a grid's second dimension: 2^16
+  if (K > 1 << 28) return unsupported("K must be at most 2^28");  // offsets of a row of blocks: 32 bits
+  const Mx4Dims d = mx4_dims(T, K);
+  if ((int64_t)d.nb * d.kb >= (int64_t)1 << 25) return unsupported("T * K must be below 2^36");
+  return SFFN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -458,6 +469,49 @@ sffn_status_t sffn_mx4_linear(const void* tiled, int32_t N, int32_t K, int32_t x
                   y_dtype == SFFN_BF16, y};
   auto f = [&] { return launch_mx4_linear(a, static_cast<hipStream_t>(stream)); };
   return api_run("mx4_linear", static_cast<hipStream_t>(stream), f);
+}
+
+sffn_status_t sffn_mx4_tokens_bytes(int32_t T, int32_t K, size_t* bytes) {
+  OPS_TRY(check_tokens(T, K));
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = mx4_dims(T, K).bytes();
+  return SFFN_OK;
+}
+
+sffn_status_t sffn_mx4_tokens(int32_t dtype, const void* x, int64_t x_stride, int32_t T, int32_t K,
+                              void* tokens, void* stream) {
+  if (dtype != SFFN_F32 && dtype != SFFN_BF16) return invalid("dtype must be SFFN_F32 or SFFN_BF16");
+  OPS_TRY(check_tokens(T, K));
+  if (T == 0) return SFFN_OK;
+  OPS_TRY(check_matrix(x, x_stride, T, K, dtype, "x is NULL", "x_stride is less than K"));
+  if (!tokens) return invalid("tokens is NULL");
+  if (misaligned(tokens, 16)) return invalid("tokens must be 16-byte aligned");
+  OPS_TRY(check_overlap({block(tokens, mx4_dims(T, K).bytes())},
+                        {matrix(x, x_stride, T, K, size_of(dtype))}));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto f = [&] { return launch_mx4_tokens(dtype == SFFN_BF16, x, x_stride, T, K, tokens, s); };
+  return api_run("mx4_tokens", s, f);
+}
+
+sffn_status_t sffn_mx4_matmul(const void* tiled, int32_t N, int32_t K, const void* tokens, int32_t T,
+                              const float* bias, int32_t relu, int32_t y_dtype, void* y, void* stream) {
+  OPS_TRY(check_mx4(N, K));
+  OPS_TRY(check_tokens(T, K));
+  if (y_dtype != SFFN_F32 && y_dtype != SFFN_BF16)
+    return invalid("y_dtype must be SFFN_F32 or SFFN_BF16");
+  if (T == 0 || N == 0) return SFFN_OK;
+  if ((int64_t)T * N > (int64_t)1 << 38) return unsupported("T * N must be at most 2^38");
+  if (!tiled || !tokens || !y) return invalid("tiled, tokens or y is NULL");
+  if (misaligned(tiled, 16) || misaligned(tokens, 16))
+    return invalid("tiled and tokens must be 16-byte aligned");
+  if (misaligned(y, size_of(y_dtype)) || misaligned(bias, 4))
+    return invalid("a pointer is not aligned to its element");
+  OPS_TRY(check_overlap({block(y, (uint64_t)T * N * size_of(y_dtype))},
+                        {block(tiled, mx4_dims(N, K).bytes()), block(tokens, mx4_dims(T, K).bytes()),
+                         block(bias, (uint64_t)N * 4)}));
+  const Mx4MatmulArgs a{tiled, mx4_dims(N, K), tokens, T, bias, relu != 0, y_dtype == SFFN_BF16, y};
+  auto f = [&] { return launch_mx4_matmul(a, static_cast<hipStream_t>(stream)); };
+  return api_run("mx4_matmul", static_cast<hipStream_t>(stream), f);
 }
 
 sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t* grads, int32_t n_grads, size_t* bytes) {

@@ -446,6 +446,23 @@ struct Mx4Args {
 };
 hipError_t launch_mx4_linear(const Mx4Args& a, hipStream_t s);
 
+// Tokens in 4 bits: blocks of 16 tokens x 128 columns, the columns first, of MX4_BLOCK bytes: 1 KB of
+// codes (lane l of a wave: token l % 16, columns 32 (l / 16) to 31 after it), then 64 scales (token by
+// token, the four groups of 32 columns).
+hipError_t launch_mx4_tokens(bool bf16, const void* x, int64_t stride, int32_t T, int32_t K,
+                             void* tokens, hipStream_t s);
+struct Mx4MatmulArgs {
+  const void* tiled;
+  Mx4Dims d;
+  const void* tokens;
+  int32_t T;
+  const float* bias;
+  bool relu;
+  bool y_bf16;
+  void* y;
+};
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s);
+
 // Gradients of one launch of the norm or of the scaling; the table travels as kernel arguments.
 // n is negated for bf16.
 constexpr int GRAD_TENSORS = 128;

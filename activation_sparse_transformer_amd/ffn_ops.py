@@ -68,6 +68,9 @@ _PROTOS = {
     "sffn_mx4_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
     "sffn_mx4_tile": [_P, _P, _I32, _I32, _P, _P],
     "sffn_mx4_linear": [_P, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _I32, _P, _P],
+    "sffn_mx4_tokens_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
+    "sffn_mx4_tokens": [_I32, _P, _I64, _I32, _I32, _P, _P],
+    "sffn_mx4_matmul": [_P, _I32, _I32, _P, _I32, _P, _I32, _I32, _P, _P],
     "sffn_grad_norm_workspace": [_P, _I32, ctypes.POINTER(_SZ)],
     "sffn_grad_norm": _GRAD_NORM,
     "sffn_grad_clip": _GRAD_NORM,
@@ -439,6 +442,43 @@ def mx4_quantize(W, stream=None):
     return codes, scales
 
 
+@functools.lru_cache(maxsize=256)
+def _tokens_bytes(T, K):
+    n = _SZ()
+    st = _lib().sffn_mx4_tokens_bytes(T, K, ctypes.byref(n))
+    if st:
+        _fail(st, "sffn_mx4_tokens_bytes")
+    return n.value
+
+
+class Mx4Tokens:
+    """Tokens x [T, K] (float32 or bfloat16; rows may be strided) rounded to 4 bits as
+    mx4_quantize rounds weights, for one or more calls of Mx4Linear.quantized.  On another
+    stream than the one they were made on, a call has to wait for them, as for any tensor."""
+
+    def __init__(self, x, stream=None):
+        f = _lib()
+        torch = f.torch
+        dev = x.device
+        if _elsewhere(f, dev, stream):
+            with _on(dev, stream, x):
+                return self.__init__(x)
+        if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("x must be a float32 or bfloat16 tensor [T, K]")
+        T, K = x.shape
+        xs = _matrix(x, "x", x.dtype, (T, K), dev)
+        data = torch.empty(_tokens_bytes(T, K), dtype=torch.uint8, device=dev)
+        st = f.sffn_mx4_tokens(f.code[x.dtype], x.data_ptr(), xs, T, K, data.data_ptr(),
+                               f.stream(dev.index))
+        if st:
+            _fail(st, "sffn_mx4_tokens")
+        self._shape, self._dtype, self._data = (T, K), x.dtype, data
+
+    shape = property(lambda self: self._shape)
+    dtype = property(lambda self: self._dtype)  # before rounding
+    device = property(lambda self: self._data.device)
+
+
 class Mx4Linear:
     """y = act(x W^T + bias) with 4-bit weights W [N, K], for batches of few tokens (serving).
 
@@ -538,6 +578,45 @@ class Mx4Linear:
                                self._bias_ptr, self.relu, f.code[dt], y.data_ptr(), s)
         if st:
             _fail(st, "sffn_mx4_linear")
+        return y
+
+    def quantized(self, x, dtype=None, y=None, stream=None):
+        """The layer with the tokens in 4 bits too (x [T, K] float32 or bfloat16 is rounded as
+        mx4_quantize rounds weights, or Mx4Tokens already are): for prompts, whose products then
+        run at the 4-bit rate, and the same function for single tokens.  y [T, N] is as in a
+        call; its default type goes by x's."""
+        f = _lib()
+        torch = f.torch
+        N, K, dev, bias = self._n, self._k, self._device, self._bias
+        if _elsewhere(f, dev, stream):
+            with _on(dev, stream, x._data if isinstance(x, Mx4Tokens) else x, y):
+                return self.quantized(x, dtype, y)
+        if self._tiled.data_ptr() != self._tiled_ptr \
+                or (bias is not None and bias.data_ptr() != self._bias_ptr):
+            self._take(self._tiled, bias)  # a storage was replaced
+        if not isinstance(x, Mx4Tokens):
+            if x.dim() != 2 or x.shape[1] != K or x.device != dev:
+                raise ValueError(f"x must be a float32 or bfloat16 tensor [T, {K}] on {dev}")
+            x = Mx4Tokens(x)
+        T = x.shape[0]
+        if x.shape[1] != K or x.device != dev:
+            raise ValueError(f"the tokens must have {K} columns and be on {dev}")
+        if y is None:
+            dt = dtype or x.dtype
+            if dt not in (torch.float32, torch.bfloat16):
+                raise ValueError("dtype must be float32 or bfloat16")
+            y = torch.empty((T, N), dtype=dt, device=dev)
+        else:
+            dt = y.dtype
+            if dt not in (torch.float32, torch.bfloat16) or dtype not in (None, dt):
+                raise ValueError("y must be float32 or bfloat16, and of `dtype`")
+            _plain(y, "y", dt, (T, N), dev)
+        s = f.stream(dev.index)
+        self._held.used_on(f, dev, s)
+        st = f.sffn_mx4_matmul(self._tiled_ptr, N, K, x._data.data_ptr(), T, self._bias_ptr,
+                               self.relu, f.code[dt], y.data_ptr(), s)
+        if st:
+            _fail(st, "sffn_mx4_matmul")
         return y
 
 

@@ -18,7 +18,7 @@
  *   - Results do not depend on timing: no call adds with atomics.
  *   - Kernel names for sffn_profile_read: rms_norm, rms_norm_fp8, rms_norm_grad,
  *     rms_norm_grad_sum, layer_norm, layer_norm_fp8, layer_norm_grad, layer_norm_grad_sum,
- *     mx4_quantize, mx4_tile, mx4_linear, grad_norm, grad_norm_sum, grad_scale, adamw. */
+ *     mx4_quantize, mx4_tile, mx4_linear, mx4_tokens, mx4_matmul, grad_norm, grad_norm_sum, grad_scale, adamw. */
 #ifndef FFN_OPS_H_
 #define FFN_OPS_H_
 
@@ -148,6 +148,27 @@ sffn_status_t sffn_mx4_tile(const uint8_t *codes, const uint8_t *scales, int32_t
 sffn_status_t sffn_mx4_linear(const void *tiled, int32_t N, int32_t K, int32_t x_dtype,
                               const void *x, int64_t x_stride, const float *x_scale, int32_t T,
                               const float *bias, int32_t relu, int32_t y_dtype, void *y,
+                              void *stream);
+
+/* (host only) Bytes of the layout of T tokens of K columns that sffn_mx4_matmul reads. */
+sffn_status_t sffn_mx4_tokens_bytes(int32_t T, int32_t K, size_t *bytes);
+
+/* Round tokens x [T, K] (SFFN_F32 or SFFN_BF16) to 4 bits as sffn_mx4_quantize rounds weights, into
+ * the layout that sffn_mx4_matmul reads: `tokens` (sffn_mx4_tokens_bytes bytes, 16-byte aligned) holds
+ * for every 16 tokens and 128 columns 1 KB of codes, then the scales.  Tokens past the last one and
+ * columns past K are zeros. */
+sffn_status_t sffn_mx4_tokens(int32_t dtype, const void *x, int64_t x_stride, int32_t T, int32_t K,
+                              void *tokens, void *stream);
+
+/* y = act(x W^T + bias) for T tokens in 4 bits (the layout of sffn_mx4_tokens for this T and K) and
+ * W [N, K] in the layout of sffn_mx4_tile.  bias [N] fp32 may be NULL; act, y and N are as in
+ * sffn_mx4_linear; T up to 2^20, K up to 2^28, T K below 2^36, T N
+ * up to 2^38.  Products are exact; the sum of 128 columns, and each
+ * addition of such sums in fp32, is off by at most two fp32 roundings of the absolute values summed,
+ * within fp32's range.  Their order depends on T, N and K alone.  A token group or a weight
+ * group with the scale 255 (NaN) makes the results that it reaches NaN. */
+sffn_status_t sffn_mx4_matmul(const void *tiled, int32_t N, int32_t K, const void *tokens,
+                              int32_t T, const float *bias, int32_t relu, int32_t y_dtype, void *y,
                               void *stream);
 
 /* One gradient: n elements of its own type (SFFN_F32 or SFFN_BF16). */
