@@ -7,7 +7,8 @@
 //
 // Both operands come in blocks of 16 rows x 128 columns (MX4_BLOCK bytes): units of 16 bytes, lane by
 // lane, lane (q, r) = 16 q + r being the one of row r.  In a block of tokens, unit (q, r) is columns 32 q to
-// 32 q + 31, as the instructions take them.  A block of weights is in the order of the few-token product
+// 32 q + 31, as the instructions take them, but for the order of its words, 8 columns each: 0, 2, 1, 3 (any
+// order is right that the weights have too; this one costs no moves).  A block of weights is in the order of the few-token product
 // of bf16 values: word g of unit (q, r) is columns 32 g + 8 q to 32 g + 8 q + 7, so what the instructions
 // want is the transpose over q and the words; swaps of lane rows give it.
 #include <utility>
@@ -212,8 +213,12 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      w[c][i][0] = s[w_at + i * 128];
-      w[c][i][1] = s[w_at + i * 128 + 16];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const u32x2 u = reinterpret_cast<const u32x2*>(s + w_at + i * 128)[k];
+        const u32x2 v = reinterpret_cast<const u32x2*>(s + w_at + i * 128 + 16)[k];
+        w[c][i][k] = u32x4{u[0], u[1], v[0], v[1]};
+      }
       ws[c][i] = sc[ws_at + i * 32];
     }
   };
@@ -236,15 +241,15 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
     __builtin_amdgcn_sched_barrier(0);
     issue(kb + 3 < kbs ? kb + 3 : kbs - 1, s);
     fragments(next, c ^ 1);
-    u32x4 wt4[NP][2];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const u32x4 u = w[c][i][0], v = w[c][i][1];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // groups 2 k (h = 0) and 2 k + 1 (h = 1)
-        const auto p = __builtin_amdgcn_permlane32_swap(u[2 * k], u[2 * k + 1], false, false);
-        const auto r = __builtin_amdgcn_permlane32_swap(v[2 * k], v[2 * k + 1], false, false);
-        wt4[i][k] = u32x4{p[0], r[0], p[1], r[1]};
+      for (int k = 0; k < 2; ++k) {
+        // words 2 k and 2 k + 1 of units 2 h and 2 h + 1: swapped, they are units 0, 2, 1, 3 of group 2 k
+        // (h = 0) and 2 k + 1 (h = 1)
+        const auto u = __builtin_amdgcn_permlane32_swap(w[c][i][k][0], w[c][i][k][1], false, false);
+        const auto v = __builtin_amdgcn_permlane32_swap(w[c][i][k][2], w[c][i][k][3], false, false);
+        w[c][i][k] = u32x4{u[0], u[1], v[0], v[1]};
       }
       ws[c][i] >>= 8 * h;
     }
@@ -253,11 +258,11 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
-      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<0>(wt4[i][0], (int)ws[c][i], x[c][t][0], (int)xs[c][t], acc[i][t]);
+      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<0>(w[c][i][0], (int)ws[c][i], x[c][t][0], (int)xs[c][t], acc[i][t]);
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
-      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<2>(wt4[i][1], (int)ws[c][i], x[c][t][1], (int)xs[c][t], acc[i][t]);
+      for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<2>(w[c][i][1], (int)ws[c][i], x[c][t][1], (int)xs[c][t], acc[i][t]);
     __builtin_amdgcn_sched_barrier(0);
   };
   issue(0, s0);
@@ -297,13 +302,13 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
 // instruction takes them (weights: swapped lane rows), and the waves' sums are added in order.
 constexpr int FEW_WAVES = 8;
 
-// The transpose over a lane's words and the four lane rows.
+// The transpose over a lane's words and the four lane rows, words 1 and 2 exchanged as in the tokens.
 __device__ __forceinline__ u32x4 transpose(u32x4 w) {
   const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
   const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
   const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
   const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  return u32x4{c[0], c[1], d[0], d[1]};
+  return u32x4{c[0], d[0], c[1], d[1]};
 }
 
 template <int TT, int RB, int KS>

@@ -53,7 +53,8 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(4), raw[i].get(5), s, 2);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(6), raw[i].get(7), s, 3);
     const int b = lane >> 4, q = (lane >> 2) & 3;
-    codes[b * 256 + (q * 16 + r) * 4 + (lane & 3)] = bad ? 0u : c;
+    const int j = lane & 3, word = j == 0 || j == 3 ? j : 3 - j;  // in the order 0, 2, 1, 3
+    codes[b * 256 + (q * 16 + r) * 4 + word] = bad ? 0u : c;
     // a group past the last column has the scale 1, as in the weights
     if ((lane & 3) == 0) scales[b * 64 + r * 4 + q] = (uint8_t)(k0 < K ? scale : 127u);
   }

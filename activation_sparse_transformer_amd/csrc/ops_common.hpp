@@ -447,8 +447,8 @@ struct Mx4Args {
 hipError_t launch_mx4_linear(const Mx4Args& a, hipStream_t s);
 
 // Tokens in 4 bits: blocks of 16 tokens x 128 columns, the columns first, of MX4_BLOCK bytes: 1 KB of
-// codes (lane l of a wave: token l % 16, columns 32 (l / 16) to 31 after it), then 64 scales (token by
-// token, the four groups of 32 columns).
+// codes (lane l of a wave: token l % 16, columns 32 (l / 16) to 31 after it, in four words of 8 in the
+// order 0, 2, 1, 3), then 64 scales (token by token, the four groups of 32 columns).
 hipError_t launch_mx4_tokens(bool bf16, const void* x, int64_t stride, int32_t T, int32_t K,
                              void* tokens, hipStream_t s);
 struct Mx4MatmulArgs {
