@@ -13,6 +13,7 @@
 // want is the transpose over q and the words; swaps of lane rows give it.
 #include <utility>
 
+#include "mx4_matmul_form.hpp"
 #include "ops_common.hpp"
 
 namespace sffn {
@@ -49,10 +50,6 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ float finish(float v, float bias, bool relu) {
-  v += bias;
-  return relu && v < 0.f ? 0.f : v;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
 }
@@ -299,8 +296,9 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
 
 // ------------------------------------------------------------------ few tokens
 // Eight waves split the columns (KS) or take further rows; every wave loads its weights and tokens as the
-// instruction takes them (weights: swapped lane rows), and the waves' sums are added in order.
-constexpr int FEW_WAVES = 8;
+// 16 x 16 x 128 instruction takes them (weights: swapped lane rows), and the waves' sums are added in
+// order.  Up to 16 tokens may come as they are (X: their type): a lane then rounds the 32 columns that
+// it holds, every wave its own, which is less than a launch and a pass over memory.
 
 // The transpose over a lane's words and the four lane rows, words 1 and 2 exchanged as in the tokens.
 __device__ __forceinline__ u32x4 transpose(u32x4 w) {
@@ -311,7 +309,50 @@ __device__ __forceinline__ u32x4 transpose(u32x4 w) {
   return u32x4{c[0], d[0], c[1], d[1]};
 }
 
-template <int TT, int RB, int KS>
+// Lane (q, r)'s part of a block of tokens: from the layout, or rounded.
+template <typename X>
+struct TokenBlock {
+  Raw8<X> v[4];
+  __device__ __forceinline__ void load(const Mx4MatmulArgs& a, int tb, int kb, int q, int r) {
+    const int64_t k0 = (int64_t)kb * 128 + 32 * q;
+    const X* p = static_cast<const X*>(a.tokens) + (int64_t)r * a.x_stride + k0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = a.d.K - k0 - 8 * j;
+      v[j].zero();
+      if (r < a.T) {
+        if (n >= 8) v[j].load(p + 8 * j);
+        else if (n > 0) v[j].load_n(p + 8 * j, (int)n);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(u32x4& codes, int& scale) const {
+    float big = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big = max_abs(big, v[j].get(e));
+    const uint32_t s = mx4_scale(big);
+    codes = u32x4{mx4_codes8(v[0], s), mx4_codes8(v[2], s), mx4_codes8(v[1], s), mx4_codes8(v[3], s)};
+    scale = (int)s;
+  }
+};
+template <>
+struct TokenBlock<void> {
+  u32x4 c;
+  int s;
+  __device__ __forceinline__ void load(const Mx4MatmulArgs& a, int tb, int kb, int q, int r) {
+    const uint8_t* p = static_cast<const uint8_t*>(a.tokens) + ((size_t)tb * a.d.kb + kb) * MX4_BLOCK;
+    c = *reinterpret_cast<const u32x4*>(p + (q * 16 + r) * 16);
+    s = p[1024 + r * 4 + q];
+  }
+  __device__ __forceinline__ void get(u32x4& codes, int& scale) const {
+    codes = c;
+    scale = s;
+  }
+};
+
+template <typename X, int TT, int RB, int KS>
 __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4MatmulArgs a) {
   constexpr int PART = RB * TT * 64;
   __shared__ f32x4 part[FEW_WAVES * PART];
@@ -319,16 +360,11 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
   const int q = lane >> 4, r = lane & 15, kbs = a.d.kb, tb = (a.T + 15) / 16;
   const int wg0 = (int)blockIdx.x * (RB * FEW_WAVES / KS), rb0 = wg0 + wave / KS * RB;
   const int tb0 = (int)blockIdx.y * TT;
-  const uint8_t *w[RB], *x[TT];
+  const uint8_t* w[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     const int i = rb0 + b < a.d.nb ? rb0 + b : a.d.nb - 1;
     w[b] = static_cast<const uint8_t*>(a.tiled) + (size_t)i * kbs * MX4_BLOCK;
-  }
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int i = tb0 + t < tb ? tb0 + t : tb - 1;
-    x[t] = static_cast<const uint8_t*>(a.tokens) + (size_t)i * kbs * MX4_BLOCK;
   }
   f32x4 acc[RB][TT];
 #pragma unroll
@@ -340,16 +376,16 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
     const size_t at = (size_t)kb * MX4_BLOCK;
     u32x4 wc[RB], xc[TT];
     int ws[RB], xs[TT];
+    TokenBlock<X> x[TT];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       wc[b] = *reinterpret_cast<const u32x4*>(w[b] + at + lane * 16);
       ws[b] = w[b][at + 1024 + r * 4 + q];
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      xc[t] = *reinterpret_cast<const u32x4*>(x[t] + at + lane * 16);
-      xs[t] = x[t][at + 1024 + r * 4 + q];
-    }
+    for (int t = 0; t < TT; ++t) x[t].load(a, tb0 + t < tb ? tb0 + t : tb - 1, kb, q, r);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) x[t].get(xc[t], xs[t]);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       const u32x4 wt = transpose(wc[b]);
@@ -362,6 +398,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
 #pragma unroll
     for (int t = 0; t < TT; ++t) part[wave * PART + (b * TT + t) * 64 + lane] = acc[b][t];
   __syncthreads();
+  // lane (q, r) of a product has rows 4 q .. 4 q + 3 for token r
   const int N = a.d.N;
   for (int i = (int)threadIdx.x; i < FEW_WAVES / KS * PART; i += FEW_WAVES * 64) {
     const int g = i / PART, at = i % PART, l = at & 63, t = (at >> 6) % TT, b = (at >> 6) / TT;
@@ -374,7 +411,10 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
     const f32x4 bias = bias4(a.bias, n, N);
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = finish(s[e], bias[e], a.relu);
+    for (int e = 0; e < 4; ++e) {
+      v[e] = s[e] + bias[e];
+      v[e] = a.relu && v[e] < 0.f ? 0.f : v[e];
+    }
     if (a.y_bf16) {
       uint16_t* y = static_cast<uint16_t*>(a.y) + tok * N + n;
       if (n + 4 <= N) {
@@ -401,46 +441,46 @@ hipError_t launch_form(const Mx4MatmulArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int TT, int RB, int KS>
+template <typename X, int TT, int RB, int KS>
 hipError_t launch_few(const Mx4MatmulArgs& a, hipStream_t s) {
   constexpr int ROWS = RB * FEW_WAVES / KS;
   const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)(((a.T + 15) / 16 + TT - 1) / TT));
-  mx4_matmul_few_kernel<TT, RB, KS><<<grid, FEW_WAVES * 64, 0, s>>>(a);
+  mx4_matmul_few_kernel<X, TT, RB, KS><<<grid, FEW_WAVES * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <typename X>
+hipError_t launch_sixteen(const Mx4MatmulArgs& a, hipStream_t s) {
+  return mx4_matmul_form(a.d.nb, a.d.kb, a.T) == MX4_FEW_1 ? launch_few<X, 1, 1, 8>(a, s)
+                                                           : launch_few<X, 1, 4, 4>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
-  const char* e = getenv("SFFN_FORM");
-  const int f = e ? atoi(e) : 0;
-  if (f == 0) {
-    if (a.T <= 16) return launch_few<1, 1, 8>(a, s);
-    if (a.T <= 32) return launch_few<2, 1, 8>(a, s);
-    if (a.T <= 64) return launch_few<4, 1, 8>(a, s);
-    const int64_t tiles = (int64_t)((a.d.nb + 15) / 16) * ((a.T + 255) / 256);
-    if (tiles < 256) return launch_form<2, 2, 2, 2>(a, s);
-    return launch_form<2, 2, 4, 2>(a, s);
-  }
+  if (a.x_dtype == SFFN_F32) return launch_sixteen<float>(a, s);
+  if (a.x_dtype == SFFN_BF16) return launch_sixteen<uint16_t>(a, s);
+  int f = mx4_matmul_form(a.d.nb, a.d.kb, a.T);
+  if (const char* e = getenv("SFFN_FORM")) f = atoi(e);
   switch (f) {
-    case 1: return launch_form<2, 2, 4, 2>(a, s);
-    case 2: return launch_form<2, 2, 2, 4>(a, s);
-    case 3: return launch_form<2, 2, 2, 2>(a, s);
-    case 4: return launch_form<2, 2, 1, 1>(a, s);
-    case 5: return launch_form<2, 2, 2, 1>(a, s);
-    case 6: return launch_form<2, 2, 4, 4>(a, s);
-    case 7: return launch_form<4, 1, 2, 2>(a, s);
-    case 8: return launch_few<4, 1, 8>(a, s);
-    case 9: return launch_few<4, 2, 8>(a, s);
-    case 10: return launch_few<4, 2, 4>(a, s);
-    case 11: return launch_few<1, 1, 8>(a, s);
-    case 12: return launch_few<1, 2, 8>(a, s);
-    case 13: return launch_few<1, 2, 4>(a, s);
-    case 14: return launch_few<1, 4, 4>(a, s);
-    case 15: return launch_few<1, 4, 8>(a, s);
-    case 16: return launch_few<1, 4, 2>(a, s);
-    case 17: return launch_few<2, 2, 8>(a, s);
-    case 18: return launch_few<2, 2, 4>(a, s);
+    case MX4_FEW_1:
+    case MX4_FEW_4: return launch_sixteen<void>(a, s);
+    case MX4_FEW_32: return launch_few<void, 2, 1, 8>(a, s);
+    case MX4_FEW_64: return launch_few<void, 4, 2, 8>(a, s);
+    case MX4_TILE_64x64: return launch_form<2, 2, 1, 1>(a, s);
+    case MX4_TILE_128x64: return launch_form<2, 2, 2, 1>(a, s);
+    case MX4_TILE_128x128: return launch_form<2, 2, 2, 2>(a, s);
+    case MX4_TILE_128x256: return launch_form<2, 2, 2, 4>(a, s);
+    case 20: return launch_few<void, 4, 1, 8>(a, s);
+    case 21: return launch_few<void, 4, 2, 4>(a, s);
+    case 22: return launch_few<void, 2, 2, 8>(a, s);
+    case 23: return launch_few<void, 2, 4, 4>(a, s);
+    case 24: return launch_few<void, 3, 2, 8>(a, s);
+    case 25: return launch_few<void, 1, 1, 8>(a, s);
+    case 26: return launch_few<void, 1, 4, 4>(a, s);
+    case 27: return launch_few<void, 1, 2, 8>(a, s);
+    case 28: return launch_few<void, 1, 2, 4>(a, s);
+    case 30: return launch_few<uint16_t, 1, 1, 8>(a, s);
   }
   return hipErrorInvalidValue;
 }

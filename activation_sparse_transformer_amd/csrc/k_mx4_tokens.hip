@@ -2,8 +2,7 @@
 // in the layout that the products of mx4_matmul read.
 //
 // A lane takes 8 consecutive values, so that a wave reads 512 columns of a row in one piece; the four
-// lanes of a group find its absolute maximum and convert (the instruction rounds to nearest-even and
-// saturates; compared with the thresholds on 4 million values at every scale).  A workgroup collects 16
+// lanes of a group find its absolute maximum and convert.  A workgroup collects 16
 // rows of four blocks of 128 columns in LDS, whose codes and scales it writes in one piece each.
 #include "ops_common.hpp"
 
@@ -41,20 +40,10 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
     for (int j = 0; j < 8; ++j) big = max_abs(big, raw[i].get(j));
     big = max_abs(big, dpp<0xB1>(big));
     big = max_abs(big, dpp<0x4E>(big));
-    // exponent of the largest value less 2 (e2m1's largest); infinity or NaN: scale 255, codes 0
-    const uint32_t bits = __float_as_uint(big);
-    const bool bad = bits >= 0x7f800000u;
-    const int e = (int)(bits >> 23) - 2;
-    const uint32_t scale = bad ? 255u : (uint32_t)(e < 0 ? 0 : e);
-    const float s = __uint_as_float(scale << 23);  // the exponent field alone counts
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(0), raw[i].get(1), s, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(2), raw[i].get(3), s, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(4), raw[i].get(5), s, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, raw[i].get(6), raw[i].get(7), s, 3);
+    const uint32_t scale = mx4_scale(big);
     const int b = lane >> 4, q = (lane >> 2) & 3;
     const int j = lane & 3, word = j == 0 || j == 3 ? j : 3 - j;  // in the order 0, 2, 1, 3
-    codes[b * 256 + (q * 16 + r) * 4 + word] = bad ? 0u : c;
+    codes[b * 256 + (q * 16 + r) * 4 + word] = mx4_codes8(raw[i], scale);
     // a group past the last column has the scale 1, as in the weights
     if ((lane & 3) == 0) scales[b * 64 + r * 4 + q] = (uint8_t)(k0 < K ? scale : 127u);
   }

@@ -262,6 +262,22 @@ sffn_status_t check_tokens(int32_t T, int32_t K) {
   return SFFN_OK;
 }
 
+// What the products of 4-bit tokens check of their weights and results.
+sffn_status_t check_product(const void* tiled, int32_t N, int32_t K, int32_t T, const float* bias,
+                            int32_t y_dtype, const void* y) {
+  OPS_TRY(check_mx4(N, K));
+  OPS_TRY(check_tokens(T, K));
+  if (y_dtype != SFFN_F32 && y_dtype != SFFN_BF16)
+    return invalid("y_dtype must be SFFN_F32 or SFFN_BF16");
+  if (T == 0 || N == 0) return SFFN_OK;
+  if ((int64_t)T * N > (int64_t)1 << 38) return unsupported("T * N must be at most 2^38");
+  if (!tiled || !y) return invalid("tiled or y is NULL");
+  if (misaligned(tiled, 16)) return invalid("tiled must be 16-byte aligned");
+  if (misaligned(y, size_of(y_dtype)) || misaligned(bias, 4))
+    return invalid("a pointer is not aligned to its element");
+  return SFFN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -495,23 +511,51 @@ sffn_status_t sffn_mx4_tokens(int32_t dtype, const void* x, int64_t x_stride, in
 
 sffn_status_t sffn_mx4_matmul(const void* tiled, int32_t N, int32_t K, const void* tokens, int32_t T,
                               const float* bias, int32_t relu, int32_t y_dtype, void* y, void* stream) {
-  OPS_TRY(check_mx4(N, K));
-  OPS_TRY(check_tokens(T, K));
-  if (y_dtype != SFFN_F32 && y_dtype != SFFN_BF16)
-    return invalid("y_dtype must be SFFN_F32 or SFFN_BF16");
+  OPS_TRY(check_product(tiled, N, K, T, bias, y_dtype, y));
   if (T == 0 || N == 0) return SFFN_OK;
-  if ((int64_t)T * N > (int64_t)1 << 38) return unsupported("T * N must be at most 2^38");
-  if (!tiled || !tokens || !y) return invalid("tiled, tokens or y is NULL");
-  if (misaligned(tiled, 16) || misaligned(tokens, 16))
-    return invalid("tiled and tokens must be 16-byte aligned");
-  if (misaligned(y, size_of(y_dtype)) || misaligned(bias, 4))
-    return invalid("a pointer is not aligned to its element");
+  if (!tokens) return invalid("tokens is NULL");
+  if (misaligned(tokens, 16)) return invalid("tokens must be 16-byte aligned");
   OPS_TRY(check_overlap({block(y, (uint64_t)T * N * size_of(y_dtype))},
                         {block(tiled, mx4_dims(N, K).bytes()), block(tokens, mx4_dims(T, K).bytes()),
                          block(bias, (uint64_t)N * 4)}));
-  const Mx4MatmulArgs a{tiled, mx4_dims(N, K), tokens, T, bias, relu != 0, y_dtype == SFFN_BF16, y};
+  const Mx4MatmulArgs a{tiled, mx4_dims(N, K), tokens, MX4_TOKENS, 0, T, bias, relu != 0,
+                        y_dtype == SFFN_BF16, y};
   auto f = [&] { return launch_mx4_matmul(a, static_cast<hipStream_t>(stream)); };
   return api_run("mx4_matmul", static_cast<hipStream_t>(stream), f);
+}
+
+sffn_status_t sffn_mx4_quantized_workspace(int32_t T, int32_t K, size_t* bytes) {
+  OPS_TRY(check_tokens(T, K));
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = T <= MX4_ROUND_T ? 0 : mx4_dims(T, K).bytes();
+  return SFFN_OK;
+}
+
+sffn_status_t sffn_mx4_quantized(const void* tiled, int32_t N, int32_t K, int32_t x_dtype,
+                                 const void* x, int64_t x_stride, int32_t T, const float* bias,
+                                 int32_t relu, int32_t y_dtype, void* y, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (x_dtype != SFFN_F32 && x_dtype != SFFN_BF16)
+    return invalid("x_dtype must be SFFN_F32 or SFFN_BF16");
+  OPS_TRY(check_product(tiled, N, K, T, bias, y_dtype, y));
+  if (T == 0 || N == 0) return SFFN_OK;
+  OPS_TRY(check_matrix(x, x_stride, T, K, x_dtype, "x is NULL", "x_stride is less than K"));
+  const bool rounded = T > MX4_ROUND_T;
+  const size_t need = rounded ? mx4_dims(T, K).bytes() : 0;
+  if (rounded && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return invalid("workspace is NULL, misaligned or too small");
+  const Rows wr = block(rounded ? workspace : nullptr, need), xr = matrix(x, x_stride, T, K, size_of(x_dtype));
+  OPS_TRY(check_overlap({block(y, (uint64_t)T * N * size_of(y_dtype)), wr},
+                        {block(tiled, mx4_dims(N, K).bytes()), xr, block(bias, (uint64_t)N * 4)}));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rounded) {
+    auto f = [&] { return launch_mx4_tokens(x_dtype == SFFN_BF16, x, x_stride, T, K, workspace, s); };
+    OPS_TRY(api_run("mx4_tokens", s, f));
+  }
+  const Mx4MatmulArgs a{tiled, mx4_dims(N, K), rounded ? workspace : x, rounded ? MX4_TOKENS : x_dtype,
+                        x_stride, T, bias, relu != 0, y_dtype == SFFN_BF16, y};
+  auto f = [&] { return launch_mx4_matmul(a, s); };
+  return api_run("mx4_matmul", s, f);
 }
 
 sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t* grads, int32_t n_grads, size_t* bytes) {

@@ -231,6 +231,26 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, float* red_a, flo
   a = lane_reduce<16>(i < waves ? red_a[first + i] : 0.f, Add());
   b = lane_reduce<16>(i < waves ? red_b[first + i] : 0.f, Add());
 }
+// A group of 32 values in 4 bits.  Its scale from the largest absolute value: the exponent less 2
+// (e2m1's largest) as it is stored, at least 0; 255 with an infinity or a NaN among the values.
+__device__ __forceinline__ uint32_t mx4_scale(float big) {
+  const uint32_t bits = __float_as_uint(big);
+  const int e = (int)(bits >> 23) - 2;
+  return bits >= 0x7f800000u ? 255u : (uint32_t)(e < 0 ? 0 : e);
+}
+// Eight values at that scale as codes, to nearest-even, saturating (the instruction reads the scale's
+// exponent field alone; compared with the thresholds of mx4_quantize on 4 million values at every
+// scale, it differs in the sign of zeros only).  A group with the scale 255 has the codes 0.
+template <typename V>
+__device__ __forceinline__ uint32_t mx4_codes8(const V& v, uint32_t scale) {
+  const float s = __uint_as_float(scale << 23);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v.get(0), v.get(1), s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v.get(2), v.get(3), s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v.get(4), v.get(5), s, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v.get(6), v.get(7), s, 3);
+  return scale == 255u ? 0u : c;
+}
 // Quotients of values up to 448 s by a positive scale s, bit for bit the divide's: the product with
 // the rounded reciprocal is a few roundings off, and one fma with its remainder corrects it
 // (P. Markstein, 1990; compared with the divide on 3.2e9 pairs, half of them next to the middle
@@ -454,13 +474,17 @@ hipError_t launch_mx4_tokens(bool bf16, const void* x, int64_t stride, int32_t T
 struct Mx4MatmulArgs {
   const void* tiled;
   Mx4Dims d;
-  const void* tokens;
+  const void* tokens;  // in 4 bits, or of x_dtype (at most MX4_ROUND_T tokens, x_stride elements apart)
+  int32_t x_dtype;     // SFFN_F32, SFFN_BF16, or MX4_TOKENS
+  int64_t x_stride;
   int32_t T;
   const float* bias;
   bool relu;
   bool y_bf16;
   void* y;
 };
+constexpr int32_t MX4_TOKENS = -1;
+constexpr int32_t MX4_ROUND_T = 16;
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s);
 
 // Gradients of one launch of the norm or of the scaling; the table travels as kernel arguments.

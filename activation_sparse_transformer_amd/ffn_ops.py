@@ -71,6 +71,8 @@ _PROTOS = {
     "sffn_mx4_tokens_bytes": [_I32, _I32, ctypes.POINTER(_SZ)],
     "sffn_mx4_tokens": [_I32, _P, _I64, _I32, _I32, _P, _P],
     "sffn_mx4_matmul": [_P, _I32, _I32, _P, _I32, _P, _I32, _I32, _P, _P],
+    "sffn_mx4_quantized_workspace": [_I32, _I32, ctypes.POINTER(_SZ)],
+    "sffn_mx4_quantized": [_P, _I32, _I32, _I32, _P, _I64, _I32, _P, _I32, _I32, _P, _P, _SZ, _P],
     "sffn_grad_norm_workspace": [_P, _I32, ctypes.POINTER(_SZ)],
     "sffn_grad_norm": _GRAD_NORM,
     "sffn_grad_clip": _GRAD_NORM,
@@ -451,6 +453,15 @@ def _tokens_bytes(T, K):
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
+def _quantized_workspace(T, K):
+    n = _SZ()
+    st = _lib().sffn_mx4_quantized_workspace(T, K, ctypes.byref(n))
+    if st:
+        _fail(st, "sffn_mx4_quantized_workspace")
+    return n.value
+
+
 class Mx4Tokens:
     """Tokens x [T, K] (float32 or bfloat16; rows may be strided) rounded to 4 bits as
     mx4_quantize rounds weights, for one or more calls of Mx4Linear.quantized.  On another
@@ -594,15 +605,14 @@ class Mx4Linear:
         if self._tiled.data_ptr() != self._tiled_ptr \
                 or (bias is not None and bias.data_ptr() != self._bias_ptr):
             self._take(self._tiled, bias)  # a storage was replaced
-        if not isinstance(x, Mx4Tokens):
-            if x.dim() != 2 or x.shape[1] != K or x.device != dev:
-                raise ValueError(f"x must be a float32 or bfloat16 tensor [T, {K}] on {dev}")
-            x = Mx4Tokens(x)
-        T = x.shape[0]
-        if x.shape[1] != K or x.device != dev:
-            raise ValueError(f"the tokens must have {K} columns and be on {dev}")
+        tokens = x._data if isinstance(x, Mx4Tokens) else None
+        xt = x.dtype
+        T = x.shape[0] if len(x.shape) == 2 else -1
+        if T < 0 or x.shape[1] != K or x.device != dev or xt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"x must be a float32 or bfloat16 tensor [T, {K}] on {dev}, or "
+                             "Mx4Tokens of one")
         if y is None:
-            dt = dtype or x.dtype
+            dt = dtype or xt
             if dt not in (torch.float32, torch.bfloat16):
                 raise ValueError("dtype must be float32 or bfloat16")
             y = torch.empty((T, N), dtype=dt, device=dev)
@@ -613,10 +623,18 @@ class Mx4Linear:
             _plain(y, "y", dt, (T, N), dev)
         s = f.stream(dev.index)
         self._held.used_on(f, dev, s)
-        st = f.sffn_mx4_matmul(self._tiled_ptr, N, K, x._data.data_ptr(), T, self._bias_ptr,
-                               self.relu, f.code[dt], y.data_ptr(), s)
+        if tokens is not None:
+            st = f.sffn_mx4_matmul(self._tiled_ptr, N, K, tokens.data_ptr(), T, self._bias_ptr,
+                                   self.relu, f.code[dt], y.data_ptr(), s)
+        else:
+            xs = _matrix(x, "x", xt, (T, K), dev)
+            nb = _quantized_workspace(T, K)
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+            st = f.sffn_mx4_quantized(self._tiled_ptr, N, K, f.code[xt], x.data_ptr(), xs, T,
+                                      self._bias_ptr, self.relu, f.code[dt], y.data_ptr(),
+                                      _ptr(ws), nb, s)
         if st:
-            _fail(st, "sffn_mx4_matmul")
+            _fail(st, "sffn_mx4_quantized" if tokens is None else "sffn_mx4_matmul")
         return y
 
 

@@ -171,6 +171,17 @@ sffn_status_t sffn_mx4_matmul(const void *tiled, int32_t N, int32_t K, const voi
                               int32_t T, const float *bias, int32_t relu, int32_t y_dtype, void *y,
                               void *stream);
 
+/* (host only) Bytes of scratch sffn_mx4_quantized needs for T tokens of K columns: 0 for up to 16. */
+sffn_status_t sffn_mx4_quantized_workspace(int32_t T, int32_t K, size_t *bytes);
+
+/* sffn_mx4_tokens and sffn_mx4_matmul in one call, with the same results: x [T, K] (SFFN_F32 or
+ * SFFN_BF16) is rounded into the workspace, or up to 16 tokens in the product itself.  workspace: as
+ * many bytes as sffn_mx4_quantized_workspace says, 16-byte aligned (NULL for 0). */
+sffn_status_t sffn_mx4_quantized(const void *tiled, int32_t N, int32_t K, int32_t x_dtype,
+                                 const void *x, int64_t x_stride, int32_t T, const float *bias,
+                                 int32_t relu, int32_t y_dtype, void *y, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
 /* One gradient: n elements of its own type (SFFN_F32 or SFFN_BF16). */
 typedef struct {
   const void *grad;
