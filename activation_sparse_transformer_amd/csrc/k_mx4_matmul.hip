@@ -21,6 +21,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
+constexpr int FEW_WAVES = 8;  // of a workgroup of the forms for few tokens
 
 // s_waitcnt for at most n vector-memory operations in flight, and for all LDS operations.
 constexpr int vmcnt(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
@@ -66,14 +67,15 @@ __device__ __forceinline__ f32x4 bias4(const float* bias, int n, int N) {
 
 // ------------------------------------------------------------------ many tokens
 // 32 x 32 x 64 products (6.1 to 6.6 PFLOP/s from registers alone, where 16 x 16 x 128 ones reach 4.3 to
-// 5.4).  WN x WT waves, each with NP pairs of blocks of weight rows by TP pairs of blocks of tokens.  The
-// operands of 128 columns are a stage of LDS, filled by direct loads two stages ahead.
+// 5.4).  2 x 2 waves, each with NP pairs of blocks of weight rows by TP pairs of blocks of tokens.  The
+// operands of 128 columns are a stage of LDS, filled by direct loads three stages ahead; a wave reads the
+// next stage's fragments while the current one's products run.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int WAVES = 4;
 
-template <int WN, int WT, int NP, int TP>
+template <int NP, int TP>
 struct Form {
-  static constexpr int WAVES = WN * WT;
-  static constexpr int NW = WN * NP * 2, TW = WT * TP * 2;  // blocks of a workgroup
+  static constexpr int NW = 2 * NP * 2, TW = 2 * TP * 2;  // blocks of a workgroup
   static constexpr int BLOCKS = NW + TW;
   static constexpr int LOADS = BLOCKS / WAVES;  // of codes, of a wave and stage; and one of scales
   static constexpr int SCALE_LOADS = (BLOCKS + 15) / 16;
@@ -81,7 +83,7 @@ struct Form {
   // where a wave turns its results: two waves' places in a stage's memory
   static constexpr int F32_PAIRS = NP >= 2 && 2 * 32 * 17 <= UNITS ? 2 : 1;
   static constexpr int REGION = 32 * ((F32_PAIRS * 8 > NP * 4 ? F32_PAIRS * 8 : NP * 4) + 1);
-  static_assert(WAVES == 4 && 2 * REGION <= UNITS, "results in LDS");
+  static_assert(2 * REGION <= UNITS, "results in LDS");
   // workgroups of a CU, by LDS and by the registers of the sums and fragments
   static constexpr int REGS = NP * TP * 16 + NP * 18 + TP * 18 + 20;
   static constexpr int BY_LDS = 160 * 1024 / (3 * UNITS * 16), BY_REGS = 512 / REGS * 4 / WAVES;
@@ -142,7 +144,8 @@ __device__ __forceinline__ void write_tile(const Mx4MatmulArgs& a, const f32x16 
         if (tok >= a.T) continue;
         Y* y = static_cast<Y*>(a.y) + tok * N + n;
         if (n + PER <= N) {
-          store_v<false>(y, o);
+          if (a.past_caches) __builtin_nontemporal_store(o, reinterpret_cast<u32x4_a2*>(y));
+          else store_v<false>(y, o);
         } else {
 #pragma unroll
           for (int e = 0; e < PER; ++e)
@@ -153,14 +156,14 @@ __device__ __forceinline__ void write_tile(const Mx4MatmulArgs& a, const f32x16 
   }
 }
 
-template <int WN, int WT, int NP, int TP>
-__global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void mx4_matmul_kernel(
+template <int NP, int TP>
+__global__ __launch_bounds__(WAVES * 64, (Form<NP, TP>::PER_CU)) void mx4_matmul_kernel(
     Mx4MatmulArgs a) {
-  typedef Form<WN, WT, NP, TP> F;
+  typedef Form<NP, TP> F;
   __shared__ u32x4 s0[F::UNITS], s1[F::UNITS], s2[F::UNITS];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int h = lane >> 5, row = lane & 31;  // lane (h, row) of a 32-row operand
-  const int wn = wave % WN, wt = wave / WN;
+  const int wn = wave & 1, wt = wave >> 1;
   const int nb = a.d.nb, kbs = a.d.kb, tb = (a.T + 15) / 16;
 
   // The tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD takes consecutive tiles,
@@ -295,9 +298,9 @@ __global__ __launch_bounds__(WN * WT * 64, (Form<WN, WT, NP, TP>::PER_CU)) void 
 }
 
 // ------------------------------------------------------------------ few tokens
-// Eight waves split the columns (KS) or take further rows; every wave loads its weights and tokens as the
-// 16 x 16 x 128 instruction takes them (weights: swapped lane rows), and the waves' sums are added in
-// order.  Up to 16 tokens may come as they are (X: their type): a lane then rounds the 32 columns that
+// Eight waves split the columns; every wave loads its weights (RB blocks of rows) and tokens (TT blocks) as
+// the 16 x 16 x 128 instruction takes them (weights: swapped lane rows), and the waves' sums are added
+// in order.  Up to 16 tokens may come as they are (X: their type): a lane then rounds the 32 columns that
 // it holds, every wave its own, which is less than a launch and a pass over memory.
 
 // The transpose over a lane's words and the four lane rows, words 1 and 2 exchanged as in the tokens.
@@ -352,13 +355,13 @@ struct TokenBlock<void> {
   }
 };
 
-template <typename X, int TT, int RB, int KS>
+template <typename X, int TT, int RB>
 __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4MatmulArgs a) {
   constexpr int PART = RB * TT * 64;
   __shared__ f32x4 part[FEW_WAVES * PART];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int q = lane >> 4, r = lane & 15, kbs = a.d.kb, tb = (a.T + 15) / 16;
-  const int wg0 = (int)blockIdx.x * (RB * FEW_WAVES / KS), rb0 = wg0 + wave / KS * RB;
+  const int rb0 = (int)blockIdx.x * RB;
   const int tb0 = (int)blockIdx.y * TT;
   const uint8_t* w[RB];
 #pragma unroll
@@ -371,8 +374,8 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int kb = wave % KS; kb < kbs; kb += KS) {
+  // (many waves hide the loads: a block's loaded one turn ahead cost occupancy and time)
+  for (int kb = wave; kb < kbs; kb += FEW_WAVES) {
     const size_t at = (size_t)kb * MX4_BLOCK;
     u32x4 wc[RB], xc[TT];
     int ws[RB], xs[TT];
@@ -400,13 +403,13 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
   __syncthreads();
   // lane (q, r) of a product has rows 4 q .. 4 q + 3 for token r
   const int N = a.d.N;
-  for (int i = (int)threadIdx.x; i < FEW_WAVES / KS * PART; i += FEW_WAVES * 64) {
-    const int g = i / PART, at = i % PART, l = at & 63, t = (at >> 6) % TT, b = (at >> 6) / TT;
-    f32x4 s = part[g * KS * PART + at];
+  for (int i = (int)threadIdx.x; i < PART; i += FEW_WAVES * 64) {
+    const int l = i & 63, t = (i >> 6) % TT, b = (i >> 6) / TT;
+    f32x4 s = part[i];
 #pragma unroll
-    for (int v = 1; v < KS; ++v) s += part[(g * KS + v) * PART + at];
+    for (int v = 1; v < FEW_WAVES; ++v) s += part[v * PART + i];
     const int64_t tok = (int64_t)(tb0 + t) * 16 + (l & 15);
-    const int n = (wg0 + g * RB + b) * 16 + (l >> 4) * 4;
+    const int n = (rb0 + b) * 16 + (l >> 4) * 4;
     if (tok >= a.T || n >= N) continue;
     const f32x4 bias = bias4(a.bias, n, N);
     float v[4];
@@ -433,56 +436,50 @@ __global__ __launch_bounds__(FEW_WAVES * 64, 2) void mx4_matmul_few_kernel(Mx4Ma
   }
 }
 
-template <int WN, int WT, int NP, int TP>
+template <int NP, int TP>
 hipError_t launch_form(const Mx4MatmulArgs& a, hipStream_t s) {
-  typedef Form<WN, WT, NP, TP> F;
+  typedef Form<NP, TP> F;
   const int64_t tn = (a.d.nb + F::NW - 1) / F::NW, tt = ((a.T + 15) / 16 + F::TW - 1) / F::TW;
-  mx4_matmul_kernel<WN, WT, NP, TP><<<dim3((unsigned)(tn * tt)), F::WAVES * 64, 0, s>>>(a);
+  mx4_matmul_kernel<NP, TP><<<dim3((unsigned)(tn * tt)), WAVES * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <typename X, int TT, int RB, int KS>
+template <typename X, int TT, int RB>
 hipError_t launch_few(const Mx4MatmulArgs& a, hipStream_t s) {
-  constexpr int ROWS = RB * FEW_WAVES / KS;
-  const dim3 grid((unsigned)((a.d.nb + ROWS - 1) / ROWS), (unsigned)(((a.T + 15) / 16 + TT - 1) / TT));
-  mx4_matmul_few_kernel<X, TT, RB, KS><<<grid, FEW_WAVES * 64, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.d.nb + RB - 1) / RB), (unsigned)(((a.T + 15) / 16 + TT - 1) / TT));
+  mx4_matmul_few_kernel<X, TT, RB><<<grid, FEW_WAVES * 64, 0, s>>>(a);
   return hipGetLastError();
 }
-
 template <typename X>
-hipError_t launch_sixteen(const Mx4MatmulArgs& a, hipStream_t s) {
-  return mx4_matmul_form(a.d.nb, a.d.kb, a.T) == MX4_FEW_1 ? launch_few<X, 1, 1, 8>(a, s)
-                                                           : launch_few<X, 1, 4, 4>(a, s);
+hipError_t launch_rounding(const Mx4MatmulArgs& a, hipStream_t s) {
+  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, true)) {
+    case MX4_FEW_16x1: return launch_few<X, 1, 1>(a, s);
+    case MX4_FEW_16x2: return launch_few<X, 1, 2>(a, s);
+    default: return launch_few<X, 1, 4>(a, s);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, hipStream_t s) {
-  if (a.x_dtype == SFFN_F32) return launch_sixteen<float>(a, s);
-  if (a.x_dtype == SFFN_BF16) return launch_sixteen<uint16_t>(a, s);
-  int f = mx4_matmul_form(a.d.nb, a.d.kb, a.T);
-  if (const char* e = getenv("SFFN_FORM")) f = atoi(e);
-  switch (f) {
-    case MX4_FEW_1:
-    case MX4_FEW_4: return launch_sixteen<void>(a, s);
-    case MX4_FEW_32: return launch_few<void, 2, 1, 8>(a, s);
-    case MX4_FEW_64: return launch_few<void, 4, 2, 8>(a, s);
-    case MX4_TILE_64x64: return launch_form<2, 2, 1, 1>(a, s);
-    case MX4_TILE_128x64: return launch_form<2, 2, 2, 1>(a, s);
-    case MX4_TILE_128x128: return launch_form<2, 2, 2, 2>(a, s);
-    case MX4_TILE_128x256: return launch_form<2, 2, 2, 4>(a, s);
-    case 20: return launch_few<void, 4, 1, 8>(a, s);
-    case 21: return launch_few<void, 4, 2, 4>(a, s);
-    case 22: return launch_few<void, 2, 2, 8>(a, s);
-    case 23: return launch_few<void, 2, 4, 4>(a, s);
-    case 24: return launch_few<void, 3, 2, 8>(a, s);
-    case 25: return launch_few<void, 1, 1, 8>(a, s);
-    case 26: return launch_few<void, 1, 4, 4>(a, s);
-    case 27: return launch_few<void, 1, 2, 8>(a, s);
-    case 28: return launch_few<void, 1, 2, 4>(a, s);
-    case 30: return launch_few<uint16_t, 1, 1, 8>(a, s);
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a0, hipStream_t s) {
+  Mx4MatmulArgs a = a0;
+  // (prompts, us a call, past the caches and through them: bf16 results of 32 MB 33 and 35, 128 MB 100 and
+  // 103, 288 MB 232 and 270; fp32 of 64 MB 40 and 37, 128 MB 75 and 66, 256 MB 123 and 130)
+  a.past_caches = a.y_bf16 || (int64_t)a.T * a.d.N > 48 << 20;
+  if (a.x_dtype == SFFN_F32) return launch_rounding<float>(a, s);
+  if (a.x_dtype == SFFN_BF16) return launch_rounding<uint16_t>(a, s);
+  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, false)) {
+    case MX4_FEW_16x1: return launch_few<void, 1, 1>(a, s);
+    case MX4_FEW_16x2: return launch_few<void, 1, 2>(a, s);
+    case MX4_FEW_32x1: return launch_few<void, 2, 1>(a, s);
+    case MX4_FEW_32x2: return launch_few<void, 2, 2>(a, s);
+    case MX4_FEW_64x2: return launch_few<void, 4, 2>(a, s);
+    case MX4_TILE_64x64: return launch_form<1, 1>(a, s);
+    case MX4_TILE_128x64: return launch_form<2, 1>(a, s);
+    case MX4_TILE_128x128: return launch_form<2, 2>(a, s);
+    case MX4_TILE_128x256: return launch_form<2, 4>(a, s);
+    default: return hipErrorInvalidValue;
   }
-  return hipErrorInvalidValue;
 }
 
 }  // namespace sffn

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_helpers import need_gpu
+from tests.mx4_matmul_forms import FORMS
 from tests.ops_helpers import rounded_from
 
 pytestmark = pytest.mark.gpu
@@ -61,11 +62,12 @@ def _to(torch, a):
     return torch.from_numpy(a).cuda()
 
 
-def _check(torch, sffn, T, N, K, x_type="bf16", y_type="f32", bias=True, relu=False, seed=0, spread=6, pad=0):
+def _check(torch, sffn, T, N, K, x_type="bf16", y_type="f32", bias=True, relu=False, seed=0, spread=6, pad=0,
+           rounding=None):
     codes, scales, x = _make(torch, T, N, K, x_type, seed, spread, pad)
     b = np.random.default_rng(seed + 1).standard_normal(N).astype(np.float32) if bias else None
     lin = sffn.Mx4Linear(_to(torch, codes), _to(torch, scales), bias=_to(torch, b) if bias else None, relu=relu, in_features=K)
-    y = lin.quantized(x, dtype=_dt(torch, y_type))
+    y = lin.quantized(x if rounding is not False else sffn.Mx4Tokens(x), dtype=_dt(torch, y_type))
     assert y.shape == (T, N) and y.dtype == _dt(torch, y_type)
     w, xq = _weights(codes, scales, K), _round4(x.cpu().double().numpy())
     ref, size = xq @ w.T, np.abs(xq) @ np.abs(w).T
@@ -90,6 +92,26 @@ TOKENS = [1, 2, 15, 16, 17, 32, 33, 48, 63, 64, 65, 100, 127, 128, 129, 255, 256
 def test_token_counts(T, N, K):
     torch, sffn = need_gpu()
     _check(torch, sffn, T, N, K, "bf16" if T % 2 else "f32", "f32" if T % 3 else "bf16", relu=T % 4 == 0, seed=T)
+
+
+@pytest.mark.parametrize("rounding,T,N,K,form", FORMS)
+@pytest.mark.parametrize("y_type", ["f32", "bf16"])
+def test_every_form(rounding, T, N, K, form, y_type):
+    """Each kernel form that the rule selects (test_mx4_matmul_form.py holds it to these sizes)."""
+    torch, sffn = need_gpu()
+    x_type = "f32" if (T + N) % 4 else "bf16"
+    lin, x, y = _check(torch, sffn, T, N, K, x_type, y_type, relu=T % 4 == 1, seed=form, rounding=rounding, pad=form % 3)
+    again = lin.quantized(sffn.Mx4Tokens(x) if rounding is not False else x, dtype=y.dtype)
+    assert torch.equal(again, y)  # rounded by the kernel or before it
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [300, 8201, 20000])
+def test_rounding_in_the_kernel(x_type, N):
+    """Both types of tokens in every form that rounds them, the last group of columns in part."""
+    torch, sffn = need_gpu()
+    for K in (5, 32, 37, 120, 130, 1007):
+        _check(torch, sffn, 7, N, K, x_type, "f32", seed=K, pad=3)
 
 
 @pytest.mark.parametrize("K", [1, 2, 31, 32, 33, 63, 65, 96, 127, 128, 129, 255, 257, 384, 500, 640, 769, 896, 1025, 4000])
