@@ -1,7 +1,10 @@
 // Host side of the C ABI declared in include/ffn_ops.h: argument checks (always before any HIP
 // call) and launches on the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "entry.hpp"
 #include "ops_common.hpp"
@@ -181,6 +184,41 @@ sffn_status_t check_grad_sizes(const sffn_grad_t* grads, int32_t n_grads) {
   return SFFN_OK;
 }
 
+// Refuses memory that is written and also read or written otherwise: the gradients (read), with `clip`
+// their outs (written; one that is its gradient itself counts once), and three blocks that are written.
+sffn_status_t check_spans(const sffn_grad_t* grads, int32_t n_grads, bool clip, const Rows (&out)[3]) {
+  struct Span {
+    uintptr_t at, end;
+    bool written;
+  };
+  constexpr int HERE = 256;
+  Span here[HERE];
+  const size_t most = (size_t)n_grads * 2 + 3;
+  std::unique_ptr<Span[]> more(most > HERE ? new (std::nothrow) Span[most] : nullptr);
+  if (most > HERE && !more) return api_fail(SFFN_ERR_DEVICE, "out of host memory");
+  Span* v = more ? more.get() : here;
+  size_t n = 0;
+  const auto add = [&](const void* p, uint64_t bytes, bool written) {
+    if (p && bytes) v[n++] = Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written};
+  };
+  for (int32_t i = 0; i < n_grads; ++i) {
+    const uint64_t bytes = (uint64_t)grads[i].n * size_of(grads[i].dtype);
+    const bool own = clip && grads[i].out == grads[i].grad;
+    add(grads[i].grad, bytes, own);
+    if (clip && !own) add(grads[i].out, bytes, true);
+  }
+  for (const Rows& r : out) add(reinterpret_cast<const void*>(r.at), r.width, true);
+  std::sort(v, v + n, [](const Span& a, const Span& b) { return a.at < b.at; });
+  uintptr_t read_to = 0, written_to = 0;
+  for (size_t i = 0; i < n; ++i) {
+    if (v[i].at < written_to || (v[i].written && v[i].at < read_to))
+      return invalid("an output overlaps an input or another output");
+    uintptr_t& to = v[i].written ? written_to : read_to;
+    if (v[i].end > to) to = v[i].end;
+  }
+  return SFFN_OK;
+}
+
 sffn_status_t grad_norm(const sffn_grad_t* grads, int32_t n_grads, double max_norm, float* norm,
                         float* factor, void* workspace, size_t workspace_bytes, bool clip,
                         void* stream) {
@@ -188,8 +226,7 @@ sffn_status_t grad_norm(const sffn_grad_t* grads, int32_t n_grads, double max_no
   if (!(max_norm >= 0.0)) return invalid("max_norm must not be negative");
   if (!norm) return invalid("norm is NULL");
   if (misaligned(norm, 4) || misaligned(factor, 4)) return invalid("a pointer is not aligned to its element");
-  const Rows nr = block(norm, 4), fr = block(factor, 4), none = block(nullptr, 0);
-  OPS_TRY(check_overlap({nr, fr}, {none}));
+  const Rows nr = block(norm, 4), fr = block(factor, 4);
   for (int32_t i = 0; i < n_grads; ++i) {
     const sffn_grad_t& g = grads[i];
     if (g.dtype != SFFN_F32 && g.dtype != SFFN_BF16) return invalid("dtype must be SFFN_F32 or SFFN_BF16");
@@ -203,14 +240,7 @@ sffn_status_t grad_norm(const sffn_grad_t* grads, int32_t n_grads, double max_no
   const size_t need = (size_t)parts * sizeof(double);
   if (parts > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
     return invalid("workspace is NULL, misaligned or too small");
-  const Rows wr = block(parts > 0 ? workspace : nullptr, need);
-  OPS_TRY(check_overlap({nr, fr, wr}, {none}));
-  for (int32_t i = 0; i < n_grads; ++i) {
-    const uint64_t bytes = (uint64_t)grads[i].n * size_of(grads[i].dtype);
-    const Rows gr = block(grads[i].grad, bytes), outr = block(clip ? grads[i].out : nullptr, bytes);
-    OPS_TRY(check_overlap({nr, fr, wr, outr}, {outr.at == gr.at ? none : gr}));
-    OPS_TRY(check_overlap({nr, fr, wr}, {gr}));
-  }
+  OPS_TRY(check_spans(grads, n_grads, clip, {nr, fr, block(parts > 0 ? workspace : nullptr, need)}));
   hipStream_t s = static_cast<hipStream_t>(stream);
   GradTable tab;
   std::memset(&tab, 0, sizeof(tab));

@@ -13,9 +13,11 @@ caller's to keep (``record_stream``) if they were allocated on a different one.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
+import itertools
 from operator import attrgetter
 
 import numpy as np
@@ -638,46 +640,33 @@ class Mx4Linear:
         return y
 
 
-def _spans(tensors):
-    return sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                  for t in tensors if t.numel())
-
-
 def _grads(grads, max_norm, out, clip, norm, factor, stream):
     f = _lib()
     torch = f.torch
     T = torch.Tensor
-    if not grads:
+    n = len(grads)
+    if not n:
         raise ValueError("no gradients")
     dev = grads[0].device
     if _elsewhere(f, dev, stream):
         with _on(dev, stream, norm, factor, *grads, *(out or ())):
             return _grads(grads, max_norm, out, clip, norm, factor, None)
-    n = len(grads)
     types = list(map(_DTYPE, grads))
-    if not set(types) <= {torch.float32, torch.bfloat16} or set(map(T.get_device, grads)) != {dev.index} \
+    kinds = set(types)
+    if not kinds <= {torch.float32, torch.bfloat16} or set(map(T.get_device, grads)) != {dev.index} \
             or not all(map(T.is_contiguous, grads)):
         raise ValueError(f"gradients must be contiguous float32 or bfloat16 tensors on {dev}")
-    ptrs = list(map(T.data_ptr, grads))
-    words = np.zeros((n, 4), dtype=np.int64)
-    words[:, 0] = ptrs
-    words[:, 2] = list(map(T.numel, grads))
-    words[:, 3] = [f.code[t] for t in types]
-    if clip:
-        if out is not None:
-            if len(out) != n or list(map(_DTYPE, out)) != types \
-                    or list(map(_SHAPE, out)) != list(map(_SHAPE, grads)) \
-                    or set(map(T.get_device, out)) != {dev.index} or not all(map(T.is_contiguous, out)):
-                raise ValueError("out must have a contiguous tensor of each gradient's shape and "
-                                 f"type, on {dev}")
-            # nothing is written over what has yet to be read or written, but a gradient by itself
-            moved = [(g, o) for g, o in zip(grads, out) if g.data_ptr() != o.data_ptr()]
-            spans = _spans([*grads, *(o for _, o in moved)]) if moved else _spans(grads)
-        else:
-            out, spans = grads, _spans(grads)
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("two of the tensors overlap")
-        words[:, 1] = list(map(T.data_ptr, out))
+    ptrs = outs = list(map(T.data_ptr, grads))
+    if out is not None:
+        if len(out) != n or list(map(_DTYPE, out)) != types \
+                or list(map(_SHAPE, out)) != list(map(_SHAPE, grads)) \
+                or set(map(T.get_device, out)) != {dev.index} or not all(map(T.is_contiguous, out)):
+            raise ValueError("out must have a contiguous tensor of each gradient's shape and type, "
+                             f"on {dev}")
+        outs = list(map(T.data_ptr, out))
+    codes = [f.code[types[0]]] * n if len(kinds) == 1 else [f.code[t] for t in types]
+    table = array.array("q", itertools.chain.from_iterable(
+        zip(ptrs, outs, map(T.numel, grads), codes)))  # an array of GradC
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:
@@ -686,15 +675,11 @@ def _grads(grads, max_norm, out, clip, norm, factor, stream):
         _plain(factor, "factor", torch.float32, (1,), dev)
     elif max_norm is not None:
         factor = torch.empty(1, dtype=torch.float32, device=dev)
-    table = words.ctypes.data
-    nb = _SZ()
-    st = f.sffn_grad_norm_workspace(table, n, ctypes.byref(nb))
-    if st:
-        _fail(st, "sffn_grad_norm_workspace")
-    ws = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    nb = 8 * (1024 + n)  # the most that the call asks for
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     fn = f.sffn_grad_clip if clip else f.sffn_grad_norm
-    st = fn(table, n, 0.0 if max_norm is None else max_norm, norm.data_ptr(), _ptr(factor),
-            ws.data_ptr(), nb.value, f.stream(dev.index))
+    st = fn(table.buffer_info()[0], n, 0.0 if max_norm is None else max_norm, norm.data_ptr(),
+            _ptr(factor), ws.data_ptr(), nb, f.stream(dev.index))
     if st:
         _fail(st, "sffn_grad_clip" if clip else "sffn_grad_norm")
     return norm, factor

@@ -192,7 +192,7 @@ typedef struct {
 } sffn_grad_t;
 
 /* (host only) Bytes of scratch sffn_grad_norm and sffn_grad_clip need for these gradients (host
- * array, of which only n is read). */
+ * array, of which only n is read): at most 8 * (1024 + n_grads). */
 sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t *grads, int32_t n_grads, size_t *bytes);
 
 /* Norm of all gradients together (host array, read before the call returns; out is not read):
@@ -210,8 +210,7 @@ sffn_status_t sffn_grad_norm(const sffn_grad_t *grads, int32_t n_grads, double m
 
 /* The same, and then out = grad * factor (rounded once to the gradient's type) for every gradient.
  * Where out is grad itself and factor is 1, nothing is written.  factor is required.  An out may be
- * its own gradient, and may overlap nothing else of its own call; the outs of different gradients,
- * and an out and another gradient, are the caller's to keep apart. */
+ * its own gradient, and may overlap nothing else of the call. */
 sffn_status_t sffn_grad_clip(const sffn_grad_t *grads, int32_t n_grads, double max_norm,
                              float *norm, float *factor, void *workspace, size_t workspace_bytes,
                              void *stream);

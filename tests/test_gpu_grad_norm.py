@@ -203,10 +203,6 @@ def test_refusals():
         lambda: sffn.clip_grads([g], 1.0, out=[g, g]),
         lambda: sffn.clip_grads([g], 1.0, out=[g.bfloat16()]),
         lambda: sffn.clip_grads([g], 1.0, out=[g[:32]]),
-        lambda: sffn.clip_grads([g, g], 1.0),
-        lambda: sffn.clip_grads([flat[:64], flat[32:96]], 1.0),
-        lambda: sffn.clip_grads([flat[:64]], 1.0, out=[flat[1:65]]),
-        lambda: sffn.clip_grads([flat[:40], flat[40:80]], 1.0, out=[flat[40:80], flat[:40]]),
         lambda: sffn.clip_grads([g, g.clone()], 1.0, out=[one, one]),
     ]
     for f in bad:
@@ -214,8 +210,16 @@ def test_refusals():
             f()
     for f in (lambda: sffn.grad_norm([g], max_norm=-1.0), lambda: sffn.grad_norm([g], max_norm=float("nan")),
               lambda: sffn.grad_norm([g], norm=g[:1]), lambda: sffn.grad_norm([g], max_norm=1.0, norm=one, factor=one),
-              lambda: sffn.clip_grads([g], 1.0, factor=g[3:4]), lambda: sffn.clip_grads([g], None)):
+              lambda: sffn.clip_grads([g], 1.0, factor=g[3:4]), lambda: sffn.clip_grads([g], None),
+              lambda: sffn.clip_grads([g, g], 1.0), lambda: sffn.clip_grads([flat[:64], flat[32:96]], 1.0),
+              lambda: sffn.clip_grads([flat[:64]], 1.0, out=[flat[1:65]]),
+              lambda: sffn.clip_grads([flat[:40], flat[40:80]], 1.0, out=[flat[40:80], flat[:40]]),
+              lambda: sffn.clip_grads([flat[i:i + 1] for i in range(100)] * 2, 1.0),
+              lambda: sffn.clip_grads([g] * 150, 1.0, out=[torch.empty_like(g) for _ in range(149)] + [g])):
         with pytest.raises(sffn.SffnError) as ei:
             f()
         assert ei.value.status == sffn.SFFN_ERR_INVALID_ARGUMENT
     assert float(sffn.grad_norm([g, g])[0]) == 0  # read only: a tensor may come twice
+    a, b = torch.empty_like(g), torch.empty_like(g)
+    sffn.clip_grads([g, g], 1.0, out=[a, b])
+    assert (a == 0).all() and (b == 0).all()

@@ -184,17 +184,83 @@ def test_grad_clip_overlap(ops, kw, call):
         assert _grad_call(ops, "sffn_grad_norm", [kw], call) == INVALID and "overlap" in _message()
 
 
+@pytest.mark.parametrize("n", [2, 130, 400])
+def test_grad_clip_overlap_between_tensors(ops, n):
+    """Of all gradients of a call, wherever in the list: what is written may meet nothing else; what is
+    only read may come twice."""
+    apart = [dict(grad=B + 4096 * i, out=B + 4096 * i) for i in range(n)]
+    last = dict(grad=9 * B, out=B + 4 * 299)  # over the first one's last element
+    for tensors in (apart + [apart[0]], apart + [dict(grad=9 * B, out=apart[n - 1]["grad"] + 1196)],
+                    [last] + apart, apart + [dict(grad=B - 1196, out=9 * B)]):
+        assert _grad_call(ops, "sffn_grad_clip", tensors, {}) == INVALID and "overlap" in _message()
+    assert _grad_call(ops, "sffn_grad_norm", apart + [dict(grad=5 * B - 1196, out=None)], {}) == INVALID
+    assert "overlap" in _message()
+
+
+MATMUL = dict(tiled=1 * B, N=48, K=64, tokens=2 * B, T=33, bias=3 * B, relu=1, y_dtype=F32, y=4 * B)
+QUANTIZED = dict(tiled=1 * B, N=48, K=64, x_dtype=BF16, x=2 * B, x_stride=64, T=33, bias=3 * B, relu=1, y_dtype=F32, y=4 * B,
+                 ws=5 * B, nb=1 << 20)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"T": 0}, OK), ({"N": 0}, OK), ({"N": -1}, INVALID), ({"K": 0}, INVALID), ({"T": -1}, INVALID),
+    ({"T": (1 << 20) + 1}, UNSUPPORTED), ({"N": 1 << 30, "K": 1 << 20}, UNSUPPORTED), ({"N": 1, "K": (1 << 28) + 1}, UNSUPPORTED),
+    ({"T": 1 << 20, "K": 1 << 17}, UNSUPPORTED), ({"T": 1 << 20, "N": (1 << 18) + 1, "K": 1}, UNSUPPORTED),
+    ({"N": (1 << 26) + 1, "K": 1}, UNSUPPORTED), ({"y_dtype": E4M3}, INVALID), ({"tiled": None}, INVALID),
+    ({"tiled": A + 8}, INVALID), ({"y": None}, INVALID), ({"y": 4 * B + 1}, INVALID), ({"bias": A + 2}, INVALID),
+])
+def test_mx4_products_arguments(ops, kw, status):
+    f = ops._lib()
+    assert f.sffn_mx4_matmul(*dict(MATMUL, **kw).values(), None) == status
+    assert f.sffn_mx4_quantized(*dict(QUANTIZED, **kw).values(), None) == status
+
+
+def test_mx4_tokens_arguments(ops):
+    f, n = ops._lib(), ctypes.c_size_t()
+    for kw in ({"tokens": None}, {"tokens": 2 * B + 8}):
+        assert f.sffn_mx4_matmul(*dict(MATMUL, **kw).values(), None) == INVALID
+    for kw in ({"x_dtype": E4M3}, {"x_dtype": 9}, {"x": None}, {"x": 2 * B + 1}, {"x_stride": 63}, {"ws": None}, {"ws": A + 8}, {"nb": 100}):
+        assert f.sffn_mx4_quantized(*dict(QUANTIZED, **kw).values(), None) == INVALID, kw
+    assert f.sffn_mx4_tokens_bytes(33, 129, ctypes.byref(n)) == OK and n.value == 3 * 2 * 1088
+    assert f.sffn_mx4_quantized_workspace(33, 129, ctypes.byref(n)) == OK and n.value == 3 * 2 * 1088
+    for T in (0, 1, 16):
+        assert f.sffn_mx4_quantized_workspace(T, 129, ctypes.byref(n)) == OK and n.value == 0
+    for fn in (f.sffn_mx4_tokens_bytes, f.sffn_mx4_quantized_workspace):
+        assert fn(33, 129, None) == INVALID and fn(-1, 129, ctypes.byref(n)) == INVALID and fn(3, 0, ctypes.byref(n)) == INVALID
+        assert fn((1 << 20) + 1, 1, ctypes.byref(n)) == UNSUPPORTED and fn(1, (1 << 28) + 1, ctypes.byref(n)) == UNSUPPORTED
+    tokens = dict(dtype=BF16, x=1 * B, x_stride=64, T=33, K=64, tokens=2 * B)
+    for kw, status in (({"T": 0, "x": None, "tokens": None}, OK), ({"dtype": E4M3}, INVALID), ({"x": None}, INVALID), ({"x": B + 1}, INVALID),
+                       ({"x_stride": 63}, INVALID), ({"tokens": None}, INVALID), ({"tokens": 2 * B + 8}, INVALID), ({"T": -1}, INVALID),
+                       ({"K": 0}, INVALID), ({"T": (1 << 20) + 1}, UNSUPPORTED)):
+        assert f.sffn_mx4_tokens(*dict(tokens, **kw).values(), None) == status, kw
+
+
+def test_mx4_tokens_overlap(ops):
+    f = ops._lib()
+    size = {"tiled": 3 * 1088, "tokens": 3 * 1088, "bias": 192, "x": 33 * 128, "ws": 3 * 1088, "y": 33 * 48 * 4}
+    for over in ("tiled", "tokens", "bias"):
+        for at in (MATMUL[over] + size[over] - 4, MATMUL[over] - size["y"] + 4):
+            assert f.sffn_mx4_matmul(*dict(MATMUL, y=at).values(), None) == INVALID and "overlap" in _message(), over
+    for out, ins in (("y", ("tiled", "x", "bias", "ws")), ("ws", ("tiled", "x", "bias"))):
+        for over in ins:
+            for at in (QUANTIZED[over] + size[over] // 16 * 16 - 16, QUANTIZED[over] - size[out] + 16):
+                assert f.sffn_mx4_quantized(*dict(QUANTIZED, **{out: at}).values(), None) == INVALID, (out, over)
+                assert "overlap" in _message(), (out, over)
+    for at in (B + 33 * 128 - 16, B - 3 * 1088 + 16):
+        assert f.sffn_mx4_tokens(BF16, B, 64, 33, 64, at, None) == INVALID and "overlap" in _message()
+
+
 def test_binding_needs_device_tensors(ops):
     import torch
     x, g = torch.zeros(2, 64), torch.ones(64)
     for call in (lambda: ops.layer_norm(x, g), lambda: ops.layer_norm_fp8(x, g),
                  lambda: ops.layer_norm_backward(x, x, g, torch.ones(2), torch.ones(2)),
-                 lambda: ops.grad_norm([x]), lambda: ops.clip_grads([x], 1.0)):
+                 lambda: ops.grad_norm([x]), lambda: ops.clip_grads([x], 1.0), lambda: ops.Mx4Tokens(x)):
         with pytest.raises(ValueError):
             call()
 
 
-@pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad", "k_grad_norm"])
+@pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad", "k_grad_norm", "k_mx4_tokens", "k_mx4_matmul"])
 def test_vector_accesses_are_declared_at_their_alignment(name):
     """As for the earlier operators: a vector access to memory of an element's alignment is written as one."""
     from activation_sparse_transformer_amd import build
