@@ -13,11 +13,9 @@ caller's to keep (``record_stream``) if they were allocated on a different one.
 """
 from __future__ import annotations
 
-import array
 import contextlib
 import ctypes
 import functools
-import itertools
 from operator import attrgetter
 
 import numpy as np
@@ -656,7 +654,7 @@ def _grads(grads, max_norm, out, clip, norm, factor, stream):
     if not kinds <= {torch.float32, torch.bfloat16} or set(map(T.get_device, grads)) != {dev.index} \
             or not all(map(T.is_contiguous, grads)):
         raise ValueError(f"gradients must be contiguous float32 or bfloat16 tensors on {dev}")
-    ptrs = outs = list(map(T.data_ptr, grads))
+    ptrs = list(map(T.data_ptr, grads))
     if out is not None:
         if len(out) != n or list(map(_DTYPE, out)) != types \
                 or list(map(_SHAPE, out)) != list(map(_SHAPE, grads)) \
@@ -664,9 +662,11 @@ def _grads(grads, max_norm, out, clip, norm, factor, stream):
             raise ValueError("out must have a contiguous tensor of each gradient's shape and type, "
                              f"on {dev}")
         outs = list(map(T.data_ptr, out))
-    codes = [f.code[types[0]]] * n if len(kinds) == 1 else [f.code[t] for t in types]
-    table = array.array("q", itertools.chain.from_iterable(
-        zip(ptrs, outs, map(T.numel, grads), codes)))  # an array of GradC
+    table = np.empty((n, 4), dtype=np.int64)  # an array of GradC
+    table[:, 0] = ptrs
+    table[:, 1] = table[:, 0] if out is None else outs
+    table[:, 2] = list(map(T.numel, grads))
+    table[:, 3] = f.code[types[0]] if len(kinds) == 1 else [f.code[t] for t in types]
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:
@@ -678,7 +678,7 @@ def _grads(grads, max_norm, out, clip, norm, factor, stream):
     nb = 8 * (1024 + n)  # the most that the call asks for
     ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     fn = f.sffn_grad_clip if clip else f.sffn_grad_norm
-    st = fn(table.buffer_info()[0], n, 0.0 if max_norm is None else max_norm, norm.data_ptr(),
+    st = fn(table.ctypes.data, n, 0.0 if max_norm is None else max_norm, norm.data_ptr(),
             _ptr(factor), ws.data_ptr(), nb, f.stream(dev.index))
     if st:
         _fail(st, "sffn_grad_clip" if clip else "sffn_grad_norm")
