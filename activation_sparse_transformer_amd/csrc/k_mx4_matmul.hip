@@ -68,10 +68,16 @@ __device__ __forceinline__ f32x4 bias4(const float* bias, int n, int N) {
 // ------------------------------------------------------------------ many tokens
 // 32 x 32 x 64 products (6.1 to 6.6 PFLOP/s from registers alone, where 16 x 16 x 128 ones reach 4.3 to
 // 5.4).  2 x 2 waves, each with NP pairs of blocks of weight rows by TP pairs of blocks of tokens.  The
-// operands of 128 columns are a stage of LDS, filled by direct loads three stages ahead; a wave reads the
+// operands of 128 columns are a stage of LDS, filled by direct loads RING stages ahead; a wave reads the
 // next stage's fragments while the current one's products run.
+//
+// 16384 x 9216 x 2304 (bf16 results) takes 210 us, 3.3 PFLOP/s; 8192 x 8192 x 8192 280 us, 3.9 PFLOP/s.  What bounds
+// it is power as much as issue: the matrix units are busy 53% of the time at 1.7 GHz, and with zeros for
+// codes the same instructions take 0.74 of the time.  Tried without gain: products and reads
+// interleaved by hand, fewer vector instructions, one wave a SIMD with 128 x 128 products (spills).
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int WAVES = 4;
+constexpr int RING = 3;  // stages in LDS (4 to 8 gained nothing: the loads are hidden)
 
 template <int NP, int TP>
 struct Form {
@@ -86,10 +92,16 @@ struct Form {
   static_assert(2 * REGION <= UNITS, "results in LDS");
   // workgroups of a CU, by LDS and by the registers of the sums and fragments
   static constexpr int REGS = NP * TP * 16 + NP * 18 + TP * 18 + 20;
-  static constexpr int BY_LDS = 160 * 1024 / (3 * UNITS * 16), BY_REGS = 512 / REGS * 4 / WAVES;
+  static constexpr int BY_LDS = 160 * 1024 / (RING * UNITS * 16), BY_REGS = 512 / REGS * 4 / WAVES;
   static constexpr int PER_CU = BY_LDS < BY_REGS ? BY_LDS : BY_REGS;
   static_assert(BLOCKS % WAVES == 0 && SCALE_LOADS <= WAVES && PER_CU >= 1, "loads of a stage");
 };
+
+// Calls f(0), f(1), ... with integral constants until one returns true.
+template <int... I, typename F>
+__device__ __forceinline__ bool until(std::integer_sequence<int, I...>, F&& f) {
+  return (f(std::integral_constant<int, I>()) || ...);
+}
 
 template <int OP>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, int sa, u32x4 b, int sb, f32x16 c) {
@@ -134,10 +146,10 @@ __device__ __forceinline__ void write_tile(const Mx4MatmulArgs& a, const f32x16 
             *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
         }
       wave_fence();
-      constexpr int TOKENS = 64 / ROW;  // of an access
+      constexpr int TOKERING = 64 / ROW;  // of an access
 #pragma unroll
-      for (int k = 0; k < 32 / TOKENS; ++k) {
-        const int r = k * TOKENS + lane / ROW, u = lane % ROW;
+      for (int k = 0; k < 32 / TOKERING; ++k) {
+        const int r = k * TOKERING + lane / ROW, u = lane % ROW;
         const u32x4 o = own[r * PITCH + u];
         const int64_t tok = tok0 + t * 32 + r;
         const int n = n0 + g * 32 + u * PER;
@@ -160,7 +172,7 @@ template <int NP, int TP>
 __global__ __launch_bounds__(WAVES * 64, (Form<NP, TP>::PER_CU)) void mx4_matmul_kernel(
     Mx4MatmulArgs a) {
   typedef Form<NP, TP> F;
-  __shared__ u32x4 s0[F::UNITS], s1[F::UNITS], s2[F::UNITS];
+  __shared__ u32x4 ring[RING][F::UNITS];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int h = lane >> 5, row = lane & 31;  // lane (h, row) of a 32-row operand
   const int wn = wave & 1, wt = wave >> 1;
@@ -231,15 +243,15 @@ __global__ __launch_bounds__(WAVES * 64, (Form<NP, TP>::PER_CU)) void mx4_matmul
       for (int e = 0; e < 16; ++e) acc[i][t][e] = 0.f;
 
   // A stage, whose fragments are in registers (set c).  Once every wave has them its buffer is free for the
-  // stage three ahead; the next stage is in when only the one after it may still be loading, and its
+  // stage RING ahead; the next stage is in when only those after it may still be loading, and its
   // fragments are read while this one's products run.  Past the end the last stage is loaded again, into
   // buffers that nothing reads.
   const auto stage = [&](int kb, u32x4* s, const u32x4* next, int c) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(vmcnt(F::LOADS + 1));
+    __builtin_amdgcn_s_waitcnt(vmcnt((RING - 2) * (F::LOADS + 1)));
     __builtin_amdgcn_s_waitcnt(LGKM0);
     __asm__ volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    issue(kb + 3 < kbs ? kb + 3 : kbs - 1, s);
+    issue(kb + RING < kbs ? kb + RING : kbs - 1, s);
     fragments(next, c ^ 1);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -265,32 +277,26 @@ __global__ __launch_bounds__(WAVES * 64, (Form<NP, TP>::PER_CU)) void mx4_matmul
       for (int t = 0; t < TP; ++t) acc[i][t] = mfma32<2>(w[c][i][1], (int)ws[c][i], x[c][t][1], (int)xs[c][t], acc[i][t]);
     __builtin_amdgcn_sched_barrier(0);
   };
-  issue(0, s0);
-  issue(1 < kbs ? 1 : 0, s1);
-  issue(2 < kbs ? 2 : kbs - 1, s2);
-  __builtin_amdgcn_s_waitcnt(vmcnt(2 * (F::LOADS + 1)));
+#pragma unroll
+  for (int i = 0; i < RING; ++i) issue(i < kbs ? i : kbs - 1, ring[i]);
+  __builtin_amdgcn_s_waitcnt(vmcnt((RING - 1) * (F::LOADS + 1)));
   __asm__ volatile("s_barrier" ::: "memory");
-  fragments(s0, 0);
-  for (int kb = 0;;) {
-    stage(kb, s0, s1, 0);
-    if (++kb == kbs) break;
-    stage(kb, s1, s2, 1);
-    if (++kb == kbs) break;
-    stage(kb, s2, s0, 0);
-    if (++kb == kbs) break;
-    stage(kb, s0, s1, 1);
-    if (++kb == kbs) break;
-    stage(kb, s1, s2, 0);
-    if (++kb == kbs) break;
-    stage(kb, s2, s0, 1);
-    if (++kb == kbs) break;
+  fragments(ring[0], 0);
+  // turns of the ring, twice where a turn changes the fragments' set, until the last stage is done
+  constexpr int TURN = RING % 2 ? 2 * RING : RING;
+  int kb = 0;
+  while (!until(std::make_integer_sequence<int, TURN>(), [&](auto i) __attribute__((always_inline)) {
+    constexpr int I = decltype(i)::value;
+    stage(kb, ring[I % RING], ring[(I + 1) % RING], I & 1);
+    return ++kb == kbs;
+  })) {
   }
   __builtin_amdgcn_s_waitcnt(vmcnt(0));  // the repeated loads land before LDS goes away
 
   // The results go through LDS, a wave's 32 tokens by 64 to 128 rows at a time, so that whole cache lines
   // are written: pieces of 32 bytes a token, as a wave holds them, took three times as long.
   __asm__ volatile("s_barrier" ::: "memory");  // the fragments of every wave are read
-  u32x4* own = (wave < 2 ? s0 : s1) + (wave & 1) * F::REGION;
+  u32x4* own = ring[wave >> 1] + (wave & 1) * F::REGION;
   const int64_t tok0 = (int64_t)(t0 + wt * TP * 2) * 16;
   const int n = (n0 + wn * NP * 2) * 16;
   if (a.y_bf16) write_tile<uint16_t, NP, TP, NP>(a, acc, own, tok0, n, lane);

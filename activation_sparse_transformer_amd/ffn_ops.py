@@ -7,7 +7,8 @@ PyTorch supplies device memory and the stream.  With ``stream=None`` a call runs
 current stream of the tensors' device; a given ``stream`` is used for the kernels and for what
 the call allocates.  Tensors made on another stream have to be ready on it (the caller's events).
 Memory is not given away before the call's work is done: that of every tensor of a call with a
-given stream, and on whatever stream a call runs that of what an ``Mx4Linear`` or ``AdamW`` holds.
+given stream, and on whatever stream a call runs that of what an ``Mx4Linear``, ``Mx4Tokens`` or
+``AdamW`` holds.
 As with PyTorch's own operations, the other tensors of a call on the current stream are the
 caller's to keep (``record_stream``) if they were allocated on a different one.
 """
@@ -484,10 +485,18 @@ class Mx4Tokens:
         if st:
             _fail(st, "sffn_mx4_tokens")
         self._shape, self._dtype, self._data = (T, K), x.dtype, data
+        self._streams = {f.stream(dev.index)}
 
     shape = property(lambda self: self._shape)
     dtype = property(lambda self: self._dtype)  # before rounding
     device = property(lambda self: self._data.device)
+
+    def used_on(self, f, device, stream):
+        """Called with each product's stream handle, which is current: the memory is kept until every one
+        of them is past it, also after the object is gone."""
+        if stream not in self._streams:
+            self._data.record_stream(f.torch.cuda.current_stream(device))
+            self._streams.add(stream)
 
 
 class Mx4Linear:
@@ -600,7 +609,7 @@ class Mx4Linear:
         torch = f.torch
         N, K, dev, bias = self._n, self._k, self._device, self._bias
         if _elsewhere(f, dev, stream):
-            with _on(dev, stream, x._data if isinstance(x, Mx4Tokens) else x, y):
+            with _on(dev, stream, None if isinstance(x, Mx4Tokens) else x, y):
                 return self.quantized(x, dtype, y)
         if self._tiled.data_ptr() != self._tiled_ptr \
                 or (bias is not None and bias.data_ptr() != self._bias_ptr):
@@ -624,6 +633,7 @@ class Mx4Linear:
         s = f.stream(dev.index)
         self._held.used_on(f, dev, s)
         if tokens is not None:
+            x.used_on(f, dev, s)
             st = f.sffn_mx4_matmul(self._tiled_ptr, N, K, tokens.data_ptr(), T, self._bias_ptr,
                                    self.relu, f.code[dt], y.data_ptr(), s)
         else:
