@@ -17,8 +17,9 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
   __shared__ uint32_t codes[SPAN * 256];
   __shared__ uint8_t scales[SPAN * 64];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
-  const int kb0 = (int)blockIdx.x * SPAN;
-  const int64_t t0 = (int64_t)blockIdx.y * 16;
+  const int spans = (kb + SPAN - 1) / SPAN;
+  const int64_t tb = blockIdx.x / (uint32_t)spans, t0 = tb * 16;
+  const int kb0 = (int)(blockIdx.x % (uint32_t)spans) * SPAN;
   const int64_t k0 = (int64_t)kb0 * 128 + lane * 8;
   const int n = K - k0 >= 8 ? 8 : K > k0 ? (int)(K - k0) : 0;
   Raw8<T> raw[4];
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
   }
   __syncthreads();
   const int b = (int)(threadIdx.x >> 6);
-  uint8_t* out = tokens + ((int64_t)blockIdx.y * kb + kb0) * MX4_BLOCK;
+  uint8_t* out = tokens + (tb * kb + kb0) * MX4_BLOCK;
   if (kb0 + b < kb)
     *reinterpret_cast<u32x4*>(out + b * MX4_BLOCK + lane * 16) =
         reinterpret_cast<const u32x4*>(codes)[threadIdx.x];
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
 hipError_t launch_mx4_tokens(bool bf16, const void* x, int64_t stride, int32_t T, int32_t K,
                              void* tokens, hipStream_t s) {
   const int kb = (int)(((int64_t)K + 127) / 128);
-  const dim3 grid((unsigned)((kb + SPAN - 1) / SPAN), (unsigned)((T + 15) / 16));
+  const dim3 grid((unsigned)((int64_t)((kb + SPAN - 1) / SPAN) * ((T + 15) / 16)));  // below 2^24
   uint8_t* out = static_cast<uint8_t*>(tokens);
   if (bf16)
     mx4_tokens_kernel<uint16_t><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(x), stride, T, K, kb, out);

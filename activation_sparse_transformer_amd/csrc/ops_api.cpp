@@ -285,7 +285,7 @@ sffn_status_t check_mx4(int32_t N, int32_t K) {
 sffn_status_t check_tokens(int32_t T, int32_t K) {
   if (T < 0) return invalid("T must not be negative");
   if (K < 1) return invalid("K must be positive");
-  if (T > 1 << 20) return unsupported("T must be at most 2^20");  // a grid's second dimension: 2^16
+  if (T > 1 << 20) return unsupported("T must be at most 2^20");
   if (K > 1 << 28) return unsupported("K must be at most 2^28");  // offsets of a row of blocks: 32 bits
   const Mx4Dims d = mx4_dims(T, K);
   if ((int64_t)d.nb * d.kb >= (int64_t)1 << 25) return unsupported("T * K must be below 2^36");
@@ -300,7 +300,7 @@ sffn_status_t check_product(const void* tiled, int32_t N, int32_t K, int32_t T, 
   if (y_dtype != SFFN_F32 && y_dtype != SFFN_BF16)
     return invalid("y_dtype must be SFFN_F32 or SFFN_BF16");
   if (T == 0 || N == 0) return SFFN_OK;
-  if ((int64_t)T * N > (int64_t)1 << 38) return unsupported("T * N must be at most 2^38");
+  if ((int64_t)T * N > (int64_t)1 << 37) return unsupported("T * N must be at most 2^37");  // 2^32 threads a launch
   if (!tiled || !y) return invalid("tiled or y is NULL");
   if (misaligned(tiled, 16)) return invalid("tiled must be 16-byte aligned");
   if (misaligned(y, size_of(y_dtype)) || misaligned(bias, 4))

@@ -163,7 +163,7 @@ sffn_status_t sffn_mx4_tokens(int32_t dtype, const void *x, int64_t x_stride, in
 /* y = act(x W^T + bias) for T tokens in 4 bits (the layout of sffn_mx4_tokens for this T and K) and
  * W [N, K] in the layout of sffn_mx4_tile.  bias [N] fp32 may be NULL; act, y and N are as in
  * sffn_mx4_linear; T up to 2^20, K up to 2^28, T K below 2^36, T N
- * up to 2^38.  Products are exact; the sum of 128 columns, and each
+ * up to 2^37.  Products are exact; the sum of 128 columns, and each
  * addition of such sums in fp32, is off by at most two fp32 roundings of the absolute values summed,
  * within fp32's range.  Their order depends on T, N and K alone.  A token group or a weight
  * group with the scale 255 (NaN) makes the results that it reaches NaN. */

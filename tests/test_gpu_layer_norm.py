@@ -123,6 +123,22 @@ def test_norm_of_rows_far_from_zero(shift, d):
     _check_norm(torch, sffn, x, None, gain, bias, "f32")
 
 
+@pytest.mark.parametrize("d", [40, 300, 2304, 20000])
+def test_fp8_codes_are_of_the_quotient(d):
+    """q = e4m3(y / scale), the quotient in fp32 of the y that the same call gives in fp32."""
+    torch, sffn = need_gpu()
+    x = _rows(torch, 50, d, torch.float32, 3, shift=2.0)
+    x[7] *= 1e-35
+    x[8] = 0
+    gain, bias = _params(torch, d, torch.float32)
+    for b in (bias, None, 1e-37 * bias):
+        y = sffn.layer_norm(x, gain, bias=b)[0].cpu()
+        q, scale, _ = sffn.layer_norm_fp8(x, gain, bias=b)
+        s = (y.abs().amax(1) / 448).clamp_min(2.0 ** -126)
+        assert torch.equal(scale.cpu(), s)
+        assert torch.equal(q.cpu().view(torch.uint8) & 127, (y / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8) & 127)
+
+
 def test_norm_special_rows():
     """Rows of zeros, of one value, tiny and large values, an infinity and a NaN: the other rows
     are untouched, and the special ones follow the formula."""

@@ -270,6 +270,25 @@ def test_no_tokens_and_no_rows():
     assert none.quantized(torch.zeros((5, 96), device="cuda")).shape == (5, 0)
 
 
+def test_the_most_tokens():
+    torch, sffn = need_gpu()
+    T = 1 << 20
+    codes, scales, x = _make(torch, 64, 40, 70, "bf16")
+    lin = sffn.Mx4Linear(_to(torch, codes), _to(torch, scales), in_features=70)
+    first = lin.quantized(x)
+    y = lin.quantized(x.repeat(T // 64, 1))
+    assert y.shape == (T, 40) and (y.view(-1, 64, 40) == first).all()
+    with pytest.raises(sffn.SffnError) as ei:
+        lin.quantized(torch.zeros((T + 1, 70), dtype=torch.bfloat16, device="cuda"))
+    assert ei.value.status == sffn.SFFN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_long_rows(T):
+    torch, sffn = need_gpu()
+    _check(torch, sffn, T, 130, 70001, "bf16", "f32", spread=3)
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^31 results, and tokens more than 2^31 elements apart."""
     torch, sffn = need_gpu()

@@ -205,7 +205,7 @@ QUANTIZED = dict(tiled=1 * B, N=48, K=64, x_dtype=BF16, x=2 * B, x_stride=64, T=
 @pytest.mark.parametrize("kw,status", [
     ({"T": 0}, OK), ({"N": 0}, OK), ({"N": -1}, INVALID), ({"K": 0}, INVALID), ({"T": -1}, INVALID),
     ({"T": (1 << 20) + 1}, UNSUPPORTED), ({"N": 1 << 30, "K": 1 << 20}, UNSUPPORTED), ({"N": 1, "K": (1 << 28) + 1}, UNSUPPORTED),
-    ({"T": 1 << 20, "K": 1 << 17}, UNSUPPORTED), ({"T": 1 << 20, "N": (1 << 18) + 1, "K": 1}, UNSUPPORTED),
+    ({"T": 1 << 20, "K": 1 << 17}, UNSUPPORTED), ({"T": 1 << 20, "N": (1 << 17) + 1, "K": 1}, UNSUPPORTED),
     ({"N": (1 << 26) + 1, "K": 1}, UNSUPPORTED), ({"y_dtype": E4M3}, INVALID), ({"tiled": None}, INVALID),
     ({"tiled": A + 8}, INVALID), ({"y": None}, INVALID), ({"y": 4 * B + 1}, INVALID), ({"bias": A + 2}, INVALID),
 ])
