@@ -458,7 +458,7 @@ hipError_t launch_few(const Mx4MatmulArgs& a, hipStream_t s) {
 }
 template <typename X>
 hipError_t launch_rounding(const Mx4MatmulArgs& a, hipStream_t s) {
-  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, true)) {
+  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, true, !a.y_bf16)) {
     case MX4_FEW_16x1: return launch_few<X, 1, 1>(a, s);
     case MX4_FEW_16x2: return launch_few<X, 1, 2>(a, s);
     default: return launch_few<X, 1, 4>(a, s);
@@ -474,7 +474,7 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a0, hipStream_t s) {
   a.past_caches = a.y_bf16 || (int64_t)a.T * a.d.N > 48 << 20;
   if (a.x_dtype == SFFN_F32) return launch_rounding<float>(a, s);
   if (a.x_dtype == SFFN_BF16) return launch_rounding<uint16_t>(a, s);
-  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, false)) {
+  switch (mx4_matmul_form(a.d.nb, a.d.kb, a.T, false, !a.y_bf16)) {
     case MX4_FEW_16x1: return launch_few<void, 1, 1>(a, s);
     case MX4_FEW_16x2: return launch_few<void, 1, 2>(a, s);
     case MX4_FEW_32x1: return launch_few<void, 2, 1>(a, s);

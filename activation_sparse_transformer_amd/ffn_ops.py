@@ -667,7 +667,7 @@ def _grads(grads, max_norm, out, clip, norm, factor, stream):
     ptrs = list(map(T.data_ptr, grads))
     if out is not None:
         if len(out) != n or list(map(_DTYPE, out)) != types \
-                or list(map(_SHAPE, out)) != list(map(_SHAPE, grads)) \
+                or not all(map(T.is_same_size, out, grads)) \
                 or set(map(T.get_device, out)) != {dev.index} or not all(map(T.is_contiguous, out)):
             raise ValueError("out must have a contiguous tensor of each gradient's shape and type, "
                              f"on {dev}")

@@ -13,7 +13,7 @@ FORMS = [
     (False, 29, 4105, 2139, 4), (False, 61, 2057, 1115, 4),
     (False, 61, 8201, 2139, 5), (False, 131, 2057, 9243, 5), (False, 205, 33, 4571, 5),
     (False, 301, 8201, 601, 6), (False, 1003, 4569, 2139, 6),
-    (False, 45, 65531, 1115, 7), (False, 77, 130001, 271, 7),
-    (False, 1501, 5333, 2139, 8), (False, 333, 9999, 1503, 8),
-    (False, 4001, 9999, 1115, 9), (False, 3001, 4569, 2139, 9),
+    (False, 61, 100003, 271, 7), (False, 301, 16393, 1115, 7),
+    (False, 1501, 5333, 2139, 8), (False, 2051, 8201, 4571, 8),
+    (False, 1999, 8151, 1115, 9), (False, 3001, 4569, 2139, 9),
 ]

@@ -13,7 +13,9 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = r"""
 #include "mx4_matmul_form.hpp"
 using namespace sffn;
-extern "C" int form(int64_t nb, int64_t kb, int64_t T, int rounding) { return mx4_matmul_form(nb, kb, T, rounding); }
+extern "C" int form(int64_t nb, int64_t kb, int64_t T, int rounding, int y_f32) {
+  return mx4_matmul_form(nb, kb, T, rounding, y_f32);
+}
 extern "C" int forms() { return MX4_FORMS; }
 // Sizes whose form is none of those for their number of tokens: row blocks one by one, then in small
 // steps up to the most that a call takes; the same for blocks of columns.
@@ -23,7 +25,7 @@ extern "C" int64_t wrong(int64_t* seen) {
   for (int64_t T : tokens)
     for (int64_t nb = 1; nb <= 1 << 22; nb += nb < 5000 ? 1 : nb / 100)
       for (int64_t kb = 1; kb <= 1 << 21 && nb * kb < 1 << 25; kb += kb < 70 ? 1 : kb / 10) {
-        const int f = mx4_matmul_form(nb, kb, T, false), r = mx4_matmul_form(nb, kb, T, true);
+        const int f = mx4_matmul_form(nb, kb, T, false, T & nb & 1), r = mx4_matmul_form(nb, kb, T, true, nb & 1);
         if (T <= 16) bad += f > MX4_FEW_16x2 || r > MX4_FEW_16x4;
         else if (T <= 32) bad += f != MX4_FEW_32x1 && f != MX4_FEW_32x2;
         else bad += f < MX4_FEW_32x2 || f >= MX4_FORMS || (f == MX4_FEW_32x2 && T > 64);
@@ -42,14 +44,15 @@ def rule(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", "-I" + csrc,
                     str(d / "rule.cpp"), "-o", str(d / "rule.so")], check=True)
     L = ctypes.CDLL(str(d / "rule.so"))
-    L.form.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int]
+    L.form.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 2
     L.wrong.restype = ctypes.c_int64
     return L
 
 
 def test_tested_sizes_select_their_forms(rule):
-    got = [(r, T, N, K, rule.form(-(-N // 16), -(-K // 128), T, r)) for r, T, N, K, _ in FORMS]
-    assert got == FORMS
+    for y_f32 in (0, 1):  # the same form for both types of results
+        got = [(r, T, N, K, rule.form(-(-N // 16), -(-K // 128), T, r, y_f32)) for r, T, N, K, _ in FORMS]
+        assert got == FORMS
     assert all(N % 16 and K % 128 and T % 16 for _, T, N, K, _ in FORMS)
 
 
