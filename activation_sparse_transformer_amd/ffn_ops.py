@@ -302,14 +302,13 @@ def _norm_workspace(rows, d):
     return n.value
 
 
-def _layer_norm(name, x, gain, bias, residual, eps, y, mean, stat, h, stream):
+def _layer_norm(fp8, x, gain, bias, residual, eps, y, mean, stat, h, stream):
     f = _lib()
     torch = f.torch
     dev, dt = x.device, x.dtype
     if _elsewhere(f, dev, stream):
         with _on(dev, stream, x, gain, bias, residual, y, mean, stat, h):
-            return _layer_norm(name, x, gain, bias, residual, eps, y, mean, stat, h, None)
-    fp8 = name == "sffn_layer_norm_fp8"
+            return _layer_norm(fp8, x, gain, bias, residual, eps, y, mean, stat, h, None)
     shape = x.shape
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
         raise ValueError("x must be a float32 or bfloat16 tensor [rows, d]")
@@ -339,12 +338,15 @@ def _layer_norm(name, x, gain, bias, residual, eps, y, mean, stat, h, stream):
             _plain(h, "h", dt, shape, dev)
         else:
             h = torch.empty_like(residual) if rs == d else residual.new_empty(shape)
-    stats = (stat.data_ptr(),) if fp8 else (mean.data_ptr(), stat.data_ptr())
-    st = getattr(f, name)(f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs,
-                          gain.data_ptr(), _ptr(bias), eps, rows, d, y.data_ptr(), *stats, _ptr(h),
-                          f.stream(dev.index))
+    args = (f.code[dt], f.code[gain.dtype], x.data_ptr(), xs, _ptr(residual), rs, gain.data_ptr(),
+            _ptr(bias), eps, rows, d, y.data_ptr())
+    if fp8:
+        st = f.sffn_layer_norm_fp8(*args, stat.data_ptr(), _ptr(h), f.stream(dev.index))
+    else:
+        st = f.sffn_layer_norm(*args, mean.data_ptr(), stat.data_ptr(), _ptr(h),
+                               f.stream(dev.index))
     if st:
-        _fail(st, name)
+        _fail(st, "sffn_layer_norm_fp8" if fp8 else "sffn_layer_norm")
     return y, x if residual is None else h, mean, stat
 
 
@@ -354,15 +356,14 @@ def layer_norm(x, gain, bias=None, residual=None, eps=1e-5, y=None, h=None, mean
     gain + bias over the rows of x [rows, d] (float32 or bfloat16; rows may be strided).  gain [d]
     has x's type or float32, bias [d] gain's type.  Returns (y, h, mean, rstd): what
     layer_norm_backward takes; h is x without a residual.  Outputs may be given as in rms_norm."""
-    return _layer_norm("sffn_layer_norm", x, gain, bias, residual, eps, y, mean, rstd, h, stream)
+    return _layer_norm(False, x, gain, bias, residual, eps, y, mean, rstd, h, stream)
 
 
 def layer_norm_fp8(x, gain, bias=None, residual=None, eps=1e-5, q=None, scale=None, h=None,
                    stream=None):
     """The layer norm for serving, its output in 8 bits as rms_norm_fp8 gives it.  Returns
     (q, scale, h)."""
-    q, h, _, scale = _layer_norm("sffn_layer_norm_fp8", x, gain, bias, residual, eps, q, None,
-                                 scale, h, stream)
+    q, h, _, scale = _layer_norm(True, x, gain, bias, residual, eps, q, None, scale, h, stream)
     return q, scale, h
 
 
