@@ -146,10 +146,10 @@ __device__ __forceinline__ void write_tile(const Mx4MatmulArgs& a, const f32x16 
             *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
         }
       wave_fence();
-      constexpr int TOKERING = 64 / ROW;  // of an access
+      constexpr int AT_ONCE = 64 / ROW;  // tokens of an access
 #pragma unroll
-      for (int k = 0; k < 32 / TOKERING; ++k) {
-        const int r = k * TOKERING + lane / ROW, u = lane % ROW;
+      for (int k = 0; k < 32 / AT_ONCE; ++k) {
+        const int r = k * AT_ONCE + lane / ROW, u = lane % ROW;
         const u32x4 o = own[r * PITCH + u];
         const int64_t tok = tok0 + t * 32 + r;
         const int n = n0 + g * 32 + u * PER;

@@ -162,11 +162,11 @@ sffn_status_t sffn_mx4_tokens(int32_t dtype, const void *x, int64_t x_stride, in
 
 /* y = act(x W^T + bias) for T tokens in 4 bits (the layout of sffn_mx4_tokens for this T and K) and
  * W [N, K] in the layout of sffn_mx4_tile.  bias [N] fp32 may be NULL; act, y and N are as in
- * sffn_mx4_linear; T up to 2^20, K up to 2^28, T K below 2^36, T N
- * up to 2^37.  Products are exact; the sum of 128 columns, and each
- * addition of such sums in fp32, is off by at most two fp32 roundings of the absolute values summed,
- * within fp32's range.  Their order depends on T, N and K alone.  A token group or a weight
- * group with the scale 255 (NaN) makes the results that it reaches NaN. */
+ * sffn_mx4_linear; T up to 2^20, K up to 2^28, T K below 2^36, T N up to 2^37.  Products are
+ * exact; the sum of 128 columns, and each addition of such sums in fp32, is off by at most two fp32
+ * roundings of the absolute values summed, within fp32's range.  Their order depends on T, N, K and
+ * y's type alone.  A token group or a weight group with the scale 255 (NaN) makes the results that it
+ * reaches NaN. */
 sffn_status_t sffn_mx4_matmul(const void *tiled, int32_t N, int32_t K, const void *tokens,
                               int32_t T, const float *bias, int32_t relu, int32_t y_dtype, void *y,
                               void *stream);
@@ -208,7 +208,7 @@ sffn_status_t sffn_grad_norm(const sffn_grad_t *grads, int32_t n_grads, double m
                              float *norm, float *factor, void *workspace, size_t workspace_bytes,
                              void *stream);
 
-/* The same, and then out = grad * factor (rounded once to the gradient's type) for every gradient.
+/* The same, and then out = grad * factor (in fp32, then rounded to the gradient's type) for every gradient.
  * Where out is grad itself and factor is 1, nothing is written.  factor is required.  An out may be
  * its own gradient, and may overlap nothing else of the call. */
 sffn_status_t sffn_grad_clip(const sffn_grad_t *grads, int32_t n_grads, double max_norm,
