@@ -30,25 +30,25 @@ MAX_WEIGHTS = 65536 * 4096
 def listed():
     return [
         # one token being decoded: the norm whose 8-bit output the 4-bit product reads
-        dict(name="layer norm: one token 8 bits", op="norm", rows=1, d=2048, dtype="bf16", residual=True, bias=True, out="fp8", pad=0),
+        dict(name="layer norm: one token, 8 bits", op="norm", rows=1, d=2048, dtype="bf16", residual=True, bias=True, out="fp8", pad=0),
         # a training batch of the 1.5B-like layer
         dict(name="layer norm: 1.5B-like batch", op="norm", rows=8192, d=2048, dtype="bf16", residual=True, bias=True, out="same", pad=0),
         # a long prompt of the 2B-like layer, served in 8 bits
-        dict(name="layer norm: 2B-like 8 bits", op="norm", rows=16384, d=2304, dtype="bf16", residual=True, bias=True, out="fp8", pad=0),
+        dict(name="layer norm: 2B-like batch, 8 bits", op="norm", rows=16384, d=2304, dtype="bf16", residual=True, bias=True, out="fp8", pad=0),
         # a small f32 run with odd sizes: rows that start at no vector's boundary
-        dict(name="layer norm gradient: odd f32", op="norm_grad", rows=333, d=1537, dtype="f32", dres=True),
+        dict(name="layer norm gradient: odd, f32", op="norm_grad", rows=333, d=1537, dtype="f32", dres=True),
         # the training batch of the 2B-like layer
         dict(name="layer norm gradient: 2B-like batch", op="norm_grad", rows=16384, d=2304, dtype="bf16", dres=True),
         # many small odd tensors, as the gains and biases of a deep model are: norm and factor for AdamW
         dict(name="gradient norm: small odd tensors", op="grads", D=0, F=0, layers=0, tensors=48, total=300007, split=7, grad="f32", clip=False, above=True, gain=1.0),
         # two 2B-like layers with the f32 gradients that the layer's backward gives
-        dict(name="gradient norm: 2B-like f32", op="grads", D=2304, F=9216, layers=2, tensors=10, total=0, split=0, grad="f32", clip=False, above=True, gain=1.0),
+        dict(name="gradient norm: 2B-like, f32", op="grads", D=2304, F=9216, layers=2, tensors=10, total=0, split=0, grad="f32", clip=False, above=True, gain=1.0),
         # one 1.5B-like layer's bf16 gradients, clipped, in the units of a scaled loss
-        dict(name="clipping: 1.5B-like bf16", op="grads", D=2048, F=8192, layers=1, tensors=5, total=0, split=0, grad="bf16", clip=True, above=True, gain=65536.0),
+        dict(name="clipping: 1.5B-like, bf16", op="grads", D=2048, F=8192, layers=1, tensors=5, total=0, split=0, grad="bf16", clip=True, above=True, gain=65536.0),
         # one token through the up-projection of the 1.5B-like layer; f32 out for the TwELL pack
         dict(name="4-bit tokens: one", op="mx4", T=1, N=8192, K=2048, x="bf16", y="f32", bias=True, relu=True, pad=0),
         # a short f32 prompt, odd numbers of tokens and rows
-        dict(name="4-bit tokens: odd f32", op="mx4", T=333, N=9999, K=1504, x="f32", y="f32", bias=True, relu=False, pad=0),
+        dict(name="4-bit tokens: odd, f32", op="mx4", T=333, N=9999, K=1504, x="f32", y="f32", bias=True, relu=False, pad=0),
         # a prompt through the up-projection of the 1.5B-like layer; f32 out for the TwELL pack
         dict(name="4-bit tokens: 1.5B-like prompt", op="mx4", T=2048, N=8192, K=2048, x="bf16", y="f32", bias=True, relu=True, pad=0),
         # the largest batch of prompts, 2B-like
