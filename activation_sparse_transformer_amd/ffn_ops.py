@@ -650,6 +650,8 @@ class Mx4Linear:
 
 
 def _grads(grads, max_norm, out, clip, norm, factor, stream):
+    if factor is not None and max_norm is None:
+        raise ValueError("factor needs max_norm")
     f = _lib()
     torch = f.torch
     T = torch.Tensor
@@ -703,15 +705,13 @@ def grad_norm(grads, max_norm=None, norm=None, factor=None, stream=None):
     what AdamW.step takes as grad_scale, with no pass over the gradients of its own.  Sums are in
     64 bits.  An infinity among the gradients gives the norm infinity and the factor 0, a NaN
     gives NaN.  norm and factor may be given."""
-    if factor is not None and max_norm is None:
-        raise ValueError("factor needs max_norm")
     return _grads(grads, max_norm, None, False, norm, factor, stream)
 
 
 def clip_grads(grads, max_norm, out=None, norm=None, factor=None, stream=None):
     """The same, and the gradients times the factor: in place, or into `out` (a list of tensors
     like grads, each of which may be its gradient itself).  The tensors written and read may not
-    overlap otherwise.  Returns (norm, factor)."""
+    overlap otherwise.  max_norm is required (None is refused).  Returns (norm, factor)."""
     return _grads(grads, max_norm, out, True, norm, factor, stream)
 
 

@@ -223,3 +223,17 @@ def test_refusals():
     a, b = torch.empty_like(g), torch.empty_like(g)
     sffn.clip_grads([g, g], 1.0, out=[a, b])
     assert (a == 0).all() and (b == 0).all()
+
+
+def test_clipping_to_no_norm_changes_nothing():
+    """None, which grad_norm takes for no clipping, is refused by a call that clips, also with a factor kept for a
+    graph: the gradients and the given tensors stay as they are."""
+    torch, sffn = need_gpu()
+    grads = _make(torch, [300, 70], [torch.float32, torch.bfloat16], 4)
+    kept, out = [t.clone() for t in grads], [torch.full_like(t, 7.0) for t in grads]
+    factor, norm = torch.full((1,), 0.5, device="cuda"), torch.full((1,), 3.0, device="cuda")
+    for kw in ({}, {"out": out}, {"norm": norm}):
+        with pytest.raises(ValueError):
+            sffn.clip_grads(grads, None, factor=factor, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(grads, kept)) and all((t == 7).all() for t in out)
+    assert float(factor) == 0.5 and float(norm) == 3

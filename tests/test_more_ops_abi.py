@@ -260,6 +260,17 @@ def test_binding_needs_device_tensors(ops):
             call()
 
 
+def test_a_factor_needs_a_norm_to_clip_to(ops):
+    """A factor without max_norm is refused before anything else of the call, by both entry points: with no norm to
+    clip to, a clipping call would scale by a factor that nobody asked for."""
+    import torch
+    x, one = torch.ones(64), torch.ones(1)
+    for call in (lambda: ops.clip_grads([x], None, factor=one), lambda: ops.clip_grads([x], None, out=[x], factor=one),
+                 lambda: ops.grad_norm([x], factor=one)):
+        with pytest.raises(ValueError, match="max_norm"):
+            call()
+
+
 @pytest.mark.parametrize("name", ["k_layer_norm", "k_layer_norm_grad", "k_grad_norm", "k_mx4_tokens", "k_mx4_matmul"])
 def test_vector_accesses_are_declared_at_their_alignment(name):
     """As for the earlier operators: a vector access to memory of an element's alignment is written as one."""
