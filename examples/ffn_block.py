@@ -32,17 +32,15 @@ class Norm:
         return [self.gain] if self.bias is None else [self.gain, self.bias]
 
     def forward(self, x, residual=None):
-        """(y, h)"""
+        """(y, h, statistics): the latter two are what backward takes."""
         if self.bias is None:
             y, h, *stats = sffn.rms_norm(x, self.gain, residual=residual)
         else:
             y, h, *stats = sffn.layer_norm(x, self.gain, bias=self.bias, residual=residual)
-        self.saved = (h, stats)
-        return y, h
+        return y, h, stats
 
-    def backward(self, dy, dres=None):
+    def backward(self, dy, h, stats, dres=None):
         """The gradient of x (and the residual), and of tensors()."""
-        h, stats = self.saved
         grad = sffn.rms_norm_backward if self.bias is None else sffn.layer_norm_backward
         dx, *grads = grad(dy, h, self.gain, *stats, dres=dres)
         return dx, grads
@@ -72,16 +70,16 @@ class Block:
         return self.norm.tensors() + [self.W_up, self.b_up, self.W_down]
 
     def forward(self, x, residual=None):
-        n, h = self.norm.forward(x, residual)
+        n, h, stats = self.norm.forward(x, residual)
         f, act = self.ffn.forward(n)
-        self.saved = (n, h, self.norm.saved, act)
+        self.saved = (n, h, stats, act)
         return f, h
 
     def backward(self, df, dh):
         """Gradients of x (and the residual) and of tensors(), from those of f and h."""
-        n, _, _, act = self.saved
+        n, h, stats, act = self.saved
         dn, dW_up, dW_down, db, _, _ = self.ffn.backward(n, df, act)
-        dx, dnorm = self.norm.backward(dn, dh)
+        dx, dnorm = self.norm.backward(dn, h, stats, dres=dh)
         return dx, dnorm + [dW_up, db, dW_down]
 
 
@@ -98,11 +96,12 @@ class Model:
         f, h = self.blocks[0].forward(x)
         for b in self.blocks[1:]:
             f, h = b.forward(f, residual=h)
-        return self.norm.forward(f, h)[0]
+        y, *self.saved = self.norm.forward(f, h)
+        return y
 
     def backward(self, dy):
         """(dx, gradients in the order of tensors())."""
-        d, grads = self.norm.backward(dy)
+        d, grads = self.norm.backward(dy, *self.saved)
         for b in reversed(self.blocks):  # d: the gradient of both f and h
             d, g = b.backward(d, d)
             grads = g + grads
@@ -120,7 +119,7 @@ class Model:
                     q, scale, h = b.norm.fp8(f, h)
                     hidden = up(q, x_scale=scale, dtype=torch.float32)
                 else:
-                    n, h = b.norm.forward(f, h)
+                    n, h, _ = b.norm.forward(f, h)
                     hidden = up.quantized(n, dtype=torch.float32)
                 f = b.ffn.down(sffn.twell_pack(b.cfg, hidden))
             return self.norm.forward(f, h)[0]

@@ -101,6 +101,25 @@ def _values(torch, codes, scales):
     return (e2m1[c] * z[:, :, None]).reshape(z.shape[0], -1)
 
 
+@pytest.mark.parametrize("layer_norm", [False, True])
+def test_serving_between_forward_and_backward(layer_norm):
+    """What is served while a training step is under way leaves that step's gradients as they are, prompts of the
+    step's own number of tokens among it."""
+    torch, _ = need_gpu()
+    from examples.ffn_block import Model
+    model = Model(tokens=96, d_model=256, d_ff=512, layer_norm=layer_norm)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, dy, other = (torch.randn((96, 256), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3))
+    model.forward(x)
+    dx, grads = model.backward(dy)
+    run = model.serve()
+    for t in (5, 64, 96):
+        model.forward(x)
+        run(other[:t])
+        dx2, grads2 = model.backward(dy)
+        assert torch.equal(dx, dx2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
+
+
 def test_a_training_step_in_a_graph():
     """Norm, its gradient, the gradients' norm and AdamW recorded while eager results live; replays on new
     inputs with eager work between give the eager step's bits."""
