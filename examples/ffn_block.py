@@ -3,8 +3,8 @@
 Training, bf16 with fp32 masters: RMS norm (or layer norm) with the residual's sum, the sparse FFN
 forward and backward, the norm's gradient, and one AdamW step over all tensors with states in 8 bits
 and the gradients clipped to a norm on the device.  Serving: the norm with its output in 8 bits, the
-up-projection in 4 bits, the TwELL pack and the sparse down-projection; prompts with the tokens in 4
-bits too.
+up-projection in 4 bits, the TwELL pack and the sparse down-projection; prompts also with the tokens in
+4 bits.
 
     python examples/ffn_block.py [--steps 40] [--tokens 512] [--d-model 512] [--d-ff 2048] [--layer-norm]
 """
@@ -107,15 +107,18 @@ class Model:
             grads = g + grads
         return d, grads
 
-    def serve(self):
-        """The forward for serving, up-projections in 4 bits laid out once: 8-bit norms for few tokens,
-        4-bit tokens for prompts."""
+    def serve(self, prompt_bits=None):
+        """The forward for serving, up-projections in 4 bits laid out once.  Up to 64 tokens are multiplied
+        in 8 bits, those of longer prompts in 8 or 4: by default 8 after RMS norms, 4 after layer norms."""
+        bits = prompt_bits or (8 if self.norm.bias is None else 4)
+        if bits not in (4, 8):
+            raise ValueError("prompt_bits must be 4 or 8")
         ups = [sffn.Mx4Linear.from_dense(b.W_up, bias=b.b_up.float(), relu=True) for b in self.blocks]
 
         def run(x):
             f, h = x, None
             for b, up in zip(self.blocks, ups):
-                if x.shape[0] <= 64:
+                if bits == 8 or x.shape[0] <= 64:
                     q, scale, h = b.norm.fp8(f, h)
                     hidden = up(q, x_scale=scale, dtype=torch.float32)
                 else:
@@ -145,7 +148,7 @@ def main(steps=40, tokens=512, d_model=512, d_ff=2048, lr=2e-3, max_norm=1.0, la
         opt.step(grads, grad_scale=factor)
     losses = torch.stack(losses).tolist()
     log(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {steps} steps")
-    run = model.serve()
+    run = model.serve(prompt_bits=4)
     y = model.forward(x).float()
     far = {}
     for t in (1, 5, 64):

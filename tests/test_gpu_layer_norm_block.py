@@ -120,6 +120,37 @@ def test_serving_between_forward_and_backward(layer_norm):
         assert torch.equal(dx, dx2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
 
 
+def test_prompts_of_blocks_with_rms_norms():
+    """Blocks with RMS norms serve any number of tokens in 8 bits unless 4 are asked for, and 4 concern prompts alone."""
+    torch, sffn = need_gpu()
+    from examples.ffn_block import Model
+    model = Model(tokens=200, d_model=256, d_ff=512)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((200, 256), generator=gen, device="cuda").to(torch.bfloat16)
+    ups = [sffn.Mx4Linear.from_dense(b.W_up, bias=b.b_up.float(), relu=True) for b in model.blocks]
+
+    def eight(x):
+        f, h = x, None
+        for b, up in zip(model.blocks, ups):
+            q, scale, h = sffn.rms_norm_fp8(f, b.norm.gain, residual=h)
+            f = b.ffn.down(sffn.twell_pack(b.cfg, up(q, x_scale=scale, dtype=torch.float32)))
+        return sffn.rms_norm(f, model.norm.gain, residual=h)[0]
+
+    def four(x):
+        f, h = x, None
+        for b, up in zip(model.blocks, ups):
+            n, h, _ = sffn.rms_norm(f, b.norm.gain, residual=h)
+            f = b.ffn.down(sffn.twell_pack(b.cfg, up.quantized(n, dtype=torch.float32)))
+        return sffn.rms_norm(f, model.norm.gain, residual=h)[0]
+    run = model.serve()
+    for t in (1, 64, 65, 200):
+        assert torch.equal(run(x[:t]), eight(x[:t]))
+    for t in (1, 64, 65, 200):
+        assert torch.equal(model.serve(prompt_bits=4)(x[:t]), (eight if t <= 64 else four)(x[:t]))
+    with pytest.raises(ValueError):
+        model.serve(prompt_bits=5)
+
+
 def test_a_training_step_in_a_graph():
     """Norm, its gradient, the gradients' norm and AdamW recorded while eager results live; replays on new
     inputs with eager work between give the eager step's bits."""
