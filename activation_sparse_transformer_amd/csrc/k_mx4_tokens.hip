@@ -14,8 +14,8 @@ constexpr int SPAN = 4;  // blocks of 128 columns of a workgroup
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t stride, int32_t rows,
                                                          int32_t K, int32_t kb, uint8_t* tokens) {
-  __shared__ uint32_t codes[SPAN * 256];
-  __shared__ uint8_t scales[SPAN * 64];
+  __shared__ u32x4 codes[SPAN * 64];  // as they are read: written by words, and the scales by bytes
+  __shared__ uint32_t scales[SPAN * 16];
   const int lane = (int)(threadIdx.x & 63), wave = uniform((int)(threadIdx.x >> 6));
   const int spans = (kb + SPAN - 1) / SPAN;
   const int64_t tb = blockIdx.x / (uint32_t)spans, t0 = tb * 16;
@@ -44,19 +44,19 @@ __global__ __launch_bounds__(256) void mx4_tokens_kernel(const T* x, int64_t str
     const uint32_t scale = mx4_scale(big);
     const int b = lane >> 4, q = (lane >> 2) & 3;
     const int j = lane & 3, word = j == 0 || j == 3 ? j : 3 - j;  // in the order 0, 2, 1, 3
-    codes[b * 256 + (q * 16 + r) * 4 + word] = mx4_codes8(raw[i], scale);
+    reinterpret_cast<uint32_t*>(codes)[b * 256 + (q * 16 + r) * 4 + word] = mx4_codes8(raw[i], scale);
     // a group past the last column has the scale 1, as in the weights
-    if ((lane & 3) == 0) scales[b * 64 + r * 4 + q] = (uint8_t)(k0 < K ? scale : 127u);
+    if ((lane & 3) == 0)
+      reinterpret_cast<uint8_t*>(scales)[b * 64 + r * 4 + q] = (uint8_t)(k0 < K ? scale : 127u);
   }
   __syncthreads();
   const int b = (int)(threadIdx.x >> 6);
   uint8_t* out = tokens + (tb * kb + kb0) * MX4_BLOCK;
   if (kb0 + b < kb)
-    *reinterpret_cast<u32x4*>(out + b * MX4_BLOCK + lane * 16) =
-        reinterpret_cast<const u32x4*>(codes)[threadIdx.x];
+    *reinterpret_cast<u32x4*>(out + b * MX4_BLOCK + lane * 16) = codes[threadIdx.x];
   if (threadIdx.x < SPAN * 16 && kb0 + (int)(threadIdx.x >> 4) < kb)
     *reinterpret_cast<uint32_t*>(out + (threadIdx.x >> 4) * MX4_BLOCK + 1024 + (threadIdx.x & 15) * 4) =
-        reinterpret_cast<const uint32_t*>(scales)[threadIdx.x];
+        scales[threadIdx.x];
 }
 
 }  // namespace

@@ -3,6 +3,7 @@ clipping, 4-bit tokens): bad arguments are refused before anything reaches the G
 a GPU."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -278,3 +279,15 @@ def test_vector_accesses_are_declared_at_their_alignment(name):
     r = subprocess.run([build.HIPCC, *build.FLAGS, "-Werror=align-mismatch", "-fsyntax-only", "--cuda-device-only",
                         os.path.join(build.CSRC, name + ".hip")], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-3000:]
+
+
+def test_lds_of_the_tokens_is_declared_as_it_is_read(tmp_path):
+    """The rounding of tokens reads its LDS in pieces of 16 bytes (codes) and 4 (scales): the arrays are declared of
+    those, so that their alignment is no matter of where the compiler puts them."""
+    from activation_sparse_transformer_amd import build
+    out = tmp_path / "tokens.ll"
+    r = subprocess.run([build.HIPCC, *build.FLAGS, "-O0", "-S", "-emit-llvm", "--cuda-device-only",
+                        os.path.join(build.CSRC, "k_mx4_tokens.hip"), "-o", str(out)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    lds = re.findall(r"\d(codes|scales) = internal addrspace\(3\) global \[\d+ x (.*?)\]", out.read_text())
+    assert len(lds) == 4 and set(lds) == {("codes", "<4 x i32>"), ("scales", "i32")}
