@@ -19,6 +19,8 @@
 namespace sffn {
 namespace {
 
+using namespace ln_grad;
+
 // Column sums of GRAD_COLUMNS columns over the rows of one of a.sum_parts parts, by a workgroup of any
 // number of waves: every 4 lanes take a row, 4 columns each; the 16 rows of a wave are joined by lane
 // rotations, the waves in LDS, in order.
@@ -260,38 +262,6 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* 
     float* out = col < d ? dgain : dbias;
     if (out) out[col < d ? col : col - d] = t;
   }
-}
-
-// Where the row groups sum the columns in registers: not above 16384 columns (they would spill), and
-// not for few rows, for which reading dy and h once more is less than a second launch.
-bool few_rows(int64_t rows, int32_t d) { return rows <= 1024 && rows * d <= 1 << 20; }
-bool sums_in_rows(int64_t rows, int32_t d) { return d <= 16384 && !few_rows(rows, d); }
-// Rows of a workgroup: as few as make 8 waves.  (With 256 workgroups, 16384 x 2304 bf16 in 2 x 5 waves
-// takes 56.4 us, in 5 69, in 3 x 5 57.4; 8192 x 4096 in 8 44.9, in 16 49.1.)
-struct GradShape {
-  RowShape row;
-  int rows;
-  int threads() const { return rows * (row.lanes > 0 ? row.lanes : 64 * row.waves); }
-};
-GradShape grad_shape(int32_t d) {
-  const RowShape r = row_shape(d, false);
-  if (r.nv > 1) return {{1024, 16, r.nv}, 1};  // (registers: a fixed number of lanes takes fewer)
-  return {r, r.lanes > 0 ? 512 / r.lanes : (8 + r.waves - 1) / r.waves};
-}
-// Workgroups of the rows: one for a CU, with equal numbers of rows.  More would write and read more
-// partial rows (16384 x 2304: 512 take 63.4 us, 384 unequally spread over the CUs 77).
-int row_groups(int64_t rows, int32_t d) {
-  const int rpb = grad_shape(d).rows;
-  const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = sums_in_rows(rows, d) ? 256 : 1 << 20;
-  const int64_t turns = (need + most - 1) / most;
-  return (int)((need + turns - 1) / turns);
-}
-// Parts of the rows whose columns other workgroups sum: one where that needs no second launch.
-int sum_parts(int64_t rows, int32_t d) {
-  if (few_rows(rows, d)) return 1;
-  const int64_t parts = (rows + 1023) / 1024;
-  return (int)(parts < 64 ? parts : 64);
 }
 
 template <typename T, typename G>

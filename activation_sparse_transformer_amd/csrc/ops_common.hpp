@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "../../include/ffn_ops.h"
+#include "layer_norm_shape.hpp"
 #include "sffn_common.hpp"
 
 namespace sffn {
@@ -356,23 +357,6 @@ hipError_t launch_rms_norm_grad(bool bf16, bool gain_f32, const NormGradArgs& a,
 hipError_t launch_rms_norm_grad_sum(const float* part, int n, int32_t d, float* dgain,
                                     hipStream_t s);
 
-// How a layer norm's kernels share a row of d elements: L lanes (16, 32, 64; several rows a
-// workgroup), or L = 0: `waves` whole waves, as many as the row's vectors of 8 need at nv a lane.
-struct RowShape {
-  int lanes, waves, nv;
-};
-constexpr int rows_of(int lanes) { return lanes == 0 ? 1 : 256 / (lanes + (lanes == 0)); }  // of 4 waves
-// wide: 16 elements a lane also where 8 would do (bf16 rows of the forward: 16384 x 2304 takes 51.8 us
-// and 45.9 with 8 bits out, 54.9 and 54.9 with 8; fp32 rows, with as many bytes in 8, lose 2%).
-inline RowShape row_shape(int32_t d, bool wide) {
-  if (d <= 128) return {16, 4, 1};
-  if (d <= 256) return {32, 4, 1};
-  if (d <= 512) return {64, 4, 1};
-  const int units = (d + 511) / 512;
-  int nv = (units + 15) / 16;
-  if (wide && nv < 2) nv = 2;
-  return {0, (units + nv - 1) / nv, nv};
-}
 // Calls f(lanes, vectors) with both as integral constants; MANY: the lanes of more than one vector.
 template <int MANY, typename F>
 hipError_t with_row_shape(const RowShape& r, F&& f) {

@@ -17,6 +17,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_helpers import need_gpu
+from tests.layer_norm_shapes import SIZES
 from tests.ops_helpers import rounded_from
 
 pytestmark = pytest.mark.gpu
@@ -338,6 +339,15 @@ def test_grad_many_rows(rows, d, dtype):
     assert none is None and torch.equal(one, dg)
     _, none, one = sffn.layer_norm_backward(dy, h, gain, mean, rstd, dres=dres, with_dgain=False)
     assert none is None and torch.equal(one, db)
+
+
+@pytest.mark.parametrize("many,few,d", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_grad_every_form(many, few, d, dtype):
+    """Every way in which the kernel shares rows and sums columns, each result against 64 bits."""
+    torch, sffn = need_gpu()
+    _check_grad(torch, sffn, many, d, dtype, dtype == "f32" or d % 2 == 0)
+    _check_grad(torch, sffn, few, d, dtype, True, False, 5)
 
 
 @pytest.mark.parametrize("d", [5, 64, 520])
