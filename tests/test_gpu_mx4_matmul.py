@@ -342,6 +342,35 @@ def test_follows_a_replaced_bias():
     assert torch.equal(lin.quantized(x, dtype=torch.float32), zero + new)
 
 
+def test_works_on_replaced_tensors():
+    """Products of 4-bit tokens take the bias and the weights as they stand, with another storage behind them too; a
+    layout that does not fit is refused.  Each expected value is of other tensors than the layer's own."""
+    torch, sffn = need_gpu()
+    for T in (7, 20, 300):  # rounded by the kernel, before it, and in tiles
+        codes, scales, x = _make(torch, T, 300, 128, "f32")
+        bias = torch.zeros(300, device="cuda")
+        lin = sffn.Mx4Linear(_to(torch, codes), _to(torch, scales), bias=bias)
+        for tokens in (x, sffn.Mx4Tokens(x)):
+            lin.bias = None
+            y0 = lin.quantized(tokens)
+            b = torch.randn(300, device="cuda")
+            lin.bias = bias
+            assert torch.equal(lin.quantized(tokens), y0)
+            bias.data = b.clone()
+            assert torch.equal(lin.quantized(tokens), y0 + b)  # (the bias's addition is one rounding in both)
+            bias.data = torch.zeros(300, device="cuda")
+            assert torch.equal(lin.quantized(tokens), y0)
+            own = lin.tiled.clone()
+            other = sffn.Mx4Linear(_to(torch, codes ^ 0x88), _to(torch, scales))  # every sign turned
+            lin.tiled.data = other.tiled.clone()
+            assert torch.equal(lin.quantized(tokens), -y0) and not torch.equal(y0, -y0)
+            lin.tiled.data = own[:-1].clone()
+            with pytest.raises(ValueError):
+                lin.quantized(tokens)
+            lin.tiled.data = own
+            assert torch.equal(lin.quantized(tokens), y0)
+
+
 def test_refusals():
     torch, sffn = need_gpu()
     lin = sffn.Mx4Linear.from_dense(torch.randn((64, 96), device="cuda"))
