@@ -8,8 +8,9 @@
 // vectors of 8 a lane) through two reductions, that of the values and that of their deviations.
 // What rounding left in the first mean, the sum of the deviations c = sum(h - mean) / d, corrects
 // both statistics: mean + c and var - c^2.  Bound by memory: 8192 x 2048 bf16 with the residual and
-// the bias moves 134 MB in 21.5 us, 16384 x 2304 302 MB in 51.5 (5.9 TB/s), with 8 bits out 264 MB in 45
-// (calls one after another into given outputs).
+// the bias moves 134 MB in 22.5 us, 16384 x 2304 302 MB in 53 (5.7 TB/s), with 8 bits out 264 MB in 47; fp32
+// 268 MB in 42.5, 604 MB in 114 (5.3 TB/s) and 491 MB in 93 (replays of calls one after another into given
+// outputs).  Above 16384 columns fewer bytes are in flight: 1024 x 32768 50 us in bf16, 122 in fp32 (4.4 TB/s).
 #include "ops_common.hpp"
 
 namespace sffn {

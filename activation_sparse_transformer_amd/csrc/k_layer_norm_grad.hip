@@ -10,10 +10,12 @@
 // order (no atomics: the result depends on the sizes alone).  Where registers do not hold the
 // column sums (above 16384 columns), or where the second launch would take longer than reading a
 // few rows twice, further workgroups of the first launch sum the columns from dy and h themselves.
-// Bound by memory: 16384 x 2304 bf16 with dres moves 302 MB in 57 us (5.3 TB/s, both launches; 62 without
-// the next row's loads in flight), 8192 x 4096 268 MB in 45.  Above 8192 columns a lane has two vectors
-// and no registers for the next row (2048 x 16384: 58 us, 4.7 TB/s; fp32 spills some), above 16384
-// dy and h are read twice (1024 x 32768: 134 us).
+// Bound by memory: 16384 x 2304 bf16 with dres moves 302 MB in 55.5 us (5.4 TB/s, both launches, replays of
+// calls one after another; in a trace their medians are 60.5 and 4.8; about 5 more without the next row's loads
+// in flight), 8192 x 4096 268 MB in 45.6; fp32 604 MB in 115 and 537 MB in 102 (5.3 TB/s).  Above 8192
+// columns a lane has two vectors and no registers for the next row (2048 x 16384: 59 us, 4.5 TB/s; fp32, which
+// spills 40 registers, 128 us, 4.2 TB/s).  Above 16384 dy and h are read twice, the second time in strips of
+// 16 columns, which in bf16 are a quarter of a line (1024 x 32768: 134 us; fp32 233).
 #include "ops_common.hpp"
 
 namespace sffn {

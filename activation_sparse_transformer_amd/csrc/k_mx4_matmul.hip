@@ -71,10 +71,12 @@ __device__ __forceinline__ f32x4 bias4(const float* bias, int n, int N) {
 // operands of 128 columns are a stage of LDS, filled by direct loads RING stages ahead; a wave reads the
 // next stage's fragments while the current one's products run.
 //
-// 16384 x 9216 x 2304 (bf16 results) takes 210 us, 3.3 PFLOP/s; 8192 x 8192 x 8192 280 us, 3.9 PFLOP/s.  What bounds
-// it is power as much as issue: the matrix units are busy 53% of the time at 1.7 GHz, and with zeros for
-// codes the same instructions take 0.74 of the time.  Tried without gain: products and reads
-// interleaved by hand, fewer vector instructions, one wave a SIMD with 128 x 128 products (spills).
+// 16384 x 9216 x 2304 (bf16 results) takes 218 us, 3.2 PFLOP/s; 8192 x 8192 x 8192 286 us, 3.8 PFLOP/s.  At the former
+// the matrix units are busy 41% of the cycles, at 1.86 GHz: a CU has 18 tiles in 9 rounds, each with about 7 us of
+// first loads and results in which they idle (65 us), and the waves wait to issue for 39% of their cycles; with
+// zeros for codes the same instructions take 0.74 of the time, so a quarter is the power of the products.  With k
+// of 16384 (2048 x 8192) they are busy 51% of the cycles, at 1.74 GHz (zeros: 0.70).  Tried without gain: products
+// and reads interleaved by hand, fewer vector instructions, one wave a SIMD with 128 x 128 products (spills).
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int WAVES = 4;
 constexpr int RING = 3;  // stages in LDS (4 to 8 gained nothing: the loads are hidden)
@@ -294,7 +296,8 @@ __global__ __launch_bounds__(WAVES * 64, (Form<NP, TP>::PER_CU)) void mx4_matmul
   __builtin_amdgcn_s_waitcnt(vmcnt(0));  // the repeated loads land before LDS goes away
 
   // The results go through LDS, a wave's 32 tokens by 64 to 128 rows at a time, so that whole cache lines
-  // are written: pieces of 32 bytes a token, as a wave holds them, took three times as long.
+  // are written where y's rows start on one: pieces of 32 bytes a token, as a wave holds them, took three times
+  // as long.
   __asm__ volatile("s_barrier" ::: "memory");  // the fragments of every wave are read
   u32x4* own = ring[wave >> 1] + (wave & 1) * F::REGION;
   const int64_t tok0 = (int64_t)(t0 + wt * TP * 2) * 16;
@@ -469,8 +472,12 @@ hipError_t launch_rounding(const Mx4MatmulArgs& a, hipStream_t s) {
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a0, hipStream_t s) {
   Mx4MatmulArgs a = a0;
-  // (prompts, us a call, past the caches and through them: bf16 results of 32 MB 33 and 35, 128 MB 100 and
-  // 103, 288 MB 232 and 270; fp32 of 64 MB 40 and 37, 128 MB 75 and 66, 256 MB 123 and 130)
+  // bf16 results of the tile forms go past the caches whatever their size, fp32 ones where they would fill them.
+  // (Prompts, us a call, past the caches and through them: bf16 results of 32 MB 33 and 35, 128 MB 100 and
+  // 103, 288 MB 232 and 270; fp32 of 64 MB 40 and 37, 128 MB 75 and 66, 256 MB 123 and 130.  Small bf16 results with
+  // a norm that reads them next, us of kernels: 1 MB 7.9 and 7.9, 4 MB 13.3 and 13.3, 16 MB 30.0 and 32.1, 32 MB
+  // 42.7 and 43.7, 72 MB 98.5 and 98.5.  Rows that start off a line, 8191 columns of 16 MB: 32.7 and 33.3, but 9217 of
+  // 72 MB: 103.5 and 98.2, the product alone 72 and 62.)
   a.past_caches = a.y_bf16 || (int64_t)a.T * a.d.N > 48 << 20;
   if (a.x_dtype == SFFN_F32) return launch_rounding<float>(a, s);
   if (a.x_dtype == SFFN_BF16) return launch_rounding<uint16_t>(a, s);

@@ -26,7 +26,10 @@ inline RowShape row_shape(int32_t d, bool wide) {
 
 namespace ln_grad {
 // Where the row groups sum the columns in registers: not above 16384 columns (they would spill), and
-// not for few rows, for which reading dy and h once more is less than a second launch.
+// not for few rows, for which reading dy and h once more is less than a second launch.  (us, bf16, read again
+// and in registers: 512 x 2048 4.8 and 10.5, 1024 x 1024 5.4 and 9.0; past the border 1024 x 2048 10.6 and 11.8,
+// 2048 x 512 6.2 and 7.0, but 2048 x 1024 13.7 and 10.1, 4096 x 128 8.0 and 6.2; fp32: 1024 x 1024 9.5 and 9.6,
+// 1024 x 2048 13.2 and 13.2, 2048 x 512 8.4 and 7.5.)
 inline bool few_rows(int64_t rows, int32_t d) { return rows <= 1024 && rows * d <= 1 << 20; }
 inline bool sums_in_rows(int64_t rows, int32_t d) { return d <= 16384 && !few_rows(rows, d); }
 // Rows of a workgroup: as few as make 8 waves.  (With 256 workgroups, 16384 x 2304 bf16 in 2 x 5 waves

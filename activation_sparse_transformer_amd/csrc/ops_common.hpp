@@ -466,7 +466,7 @@ struct Mx4MatmulArgs {
   bool relu;
   bool y_bf16;
   void* y;
-  bool past_caches;  // the launcher's: results that would fill the caches are written past them
+  bool past_caches;  // the launcher's: bf16 results, and fp32 ones that would fill the caches, go past them
 };
 constexpr int32_t MX4_TOKENS = -1;
 constexpr int32_t MX4_ROUND_T = 16;

@@ -703,8 +703,8 @@ def grad_norm(grads, max_norm=None, norm=None, factor=None, stream=None):
     together, and with max_norm the factor that clips them to it: 1, or max_norm / norm above it.
     Returns (norm, factor), float32 [1] on the device (factor None without max_norm): factor is
     what AdamW.step takes as grad_scale, with no pass over the gradients of its own.  Sums are in
-    64 bits.  An infinity among the gradients gives the norm infinity and the factor 0, a NaN
-    gives NaN.  norm and factor may be given."""
+    64 bits.  An infinity among the gradients, or a norm beyond float32, gives the norm infinity
+    and the factor 0, a NaN gives NaN.  norm and factor may be given."""
     return _grads(grads, max_norm, None, False, norm, factor, stream)
 
 

@@ -84,7 +84,8 @@ sffn_status_t sffn_rms_norm_backward(int32_t dtype, int32_t gain_dtype, const vo
  *   h = x + residual  (h = x without one),  mean = mean(h),
  *   rstd = 1 / sqrt(mean((h - mean)^2) + eps),  y = (h - mean) * rstd * gain + bias
  * in fp32, from the unrounded h; the deviations are taken from the mean of the row's own values (no
- * difference of two large sums), and their sum corrects that mean.  Types, strides and what may be
+ * difference of two large sums), and their sum corrects that mean.  A row whose sum or whose deviations'
+ * squares pass fp32's range has an infinite mean or variance, and what follows from it.  Types, strides and what may be
  * NULL are as in sffn_rms_norm; gain and bias [d] have gain_dtype, bias may be NULL (0).
  * mean and rstd [rows] fp32 may each be NULL. */
 sffn_status_t sffn_layer_norm(int32_t dtype, int32_t gain_dtype, const void *x, int64_t x_stride,
@@ -105,7 +106,8 @@ sffn_status_t sffn_layer_norm_backward_workspace(int64_t rows, int32_t d, size_t
 /* Gradient of sffn_layer_norm.  With xh = (h - mean) * rstd and t = dy * gain:
  *   dx = rstd * (t - mean(t) - xh * mean(t * xh)) + dres,
  *   dgain = sum over rows of dy * xh,   dbias = sum over rows of dy
- * h, mean and rstd are the forward's.  dgain and dbias [d] are fp32 and may each be NULL; with zero
+ * h, mean and rstd are the forward's, as stored: in a row whose mean is many times its spread, mean's
+ * rounding to fp32 puts xh off by up to 2^-24 |mean| rstd.  dgain and dbias [d] are fp32 and may each be NULL; with zero
  * rows they are cleared.  All else is as in sffn_rms_norm_backward. */
 sffn_status_t sffn_layer_norm_backward(int32_t dtype, int32_t gain_dtype, const void *dy,
                                        int64_t dy_stride, const void *h, int64_t h_stride,
@@ -200,9 +202,9 @@ sffn_status_t sffn_grad_norm_workspace(const sffn_grad_t *grads, int32_t n_grads
  *   factor[0] = 1 if norm <= max_norm, else max_norm / norm
  * with the squares, exact in 64 bits, summed in 64 bits, so that no square overflows or vanishes;
  * norm is rounded to fp32 once, and so is the quotient, by that norm.  factor is what
- * sffn_adamw_step takes as grad_scale; it may be NULL.  An infinity among the gradients gives the
- * norm infinity and, with a finite max_norm, the factor 0; a NaN gives NaN for both.  No gradients, or none with elements,
- * have the norm 0.  The order of the sums depends on the sizes alone.  workspace: as many bytes as
+ * sffn_adamw_step takes as grad_scale; it may be NULL.  An infinity among the gradients, or a norm
+ * beyond fp32's range, gives the norm infinity and, with a finite max_norm, the factor 0; a NaN gives
+ * NaN for both.  No gradients, or none with elements, have the norm 0.  The order of the sums depends on the sizes alone.  workspace: as many bytes as
  * sffn_grad_norm_workspace says, 16-byte aligned. */
 sffn_status_t sffn_grad_norm(const sffn_grad_t *grads, int32_t n_grads, double max_norm,
                              float *norm, float *factor, void *workspace, size_t workspace_bytes,
