@@ -289,6 +289,30 @@ def test_long_rows(T):
     _check(torch, sffn, T, 130, 70001, "bf16", "f32", spread=3)
 
 
+def test_the_longest_rows():
+    """2^28 columns, a row of blocks of more than 2^31 bytes: zeros but for few columns on both sides of its middle,
+    of values that 4 bits hold, so that the sums are exact."""
+    torch, sffn = need_gpu()
+    N, K = 9, 1 << 28
+    columns = [0, 5, 31, 127, 128, (1 << 27) - 1, 1 << 27, 252_645_136, 252_645_137, K - 33, K - 1]
+    rng = np.random.default_rng(4)
+    value = rng.integers(0, 16, (N, len(columns)))
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    for j, c in enumerate(columns):
+        codes[:, c // 2] |= torch.from_numpy((value[:, j] << (4 * (c % 2))).astype(np.uint8)).cuda()
+    lin = sffn.Mx4Linear(codes, torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda"))
+    del codes
+    assert lin.tiled.numel() > 1 << 31
+    x = torch.zeros((17, K), dtype=torch.bfloat16, device="cuda")
+    v = 2.0 ** rng.integers(0, 3, (17, len(columns))) * rng.choice([-1, 1], (17, len(columns)))
+    for j, c in enumerate(columns):
+        x[:, c] = torch.from_numpy(v[:, j]).cuda().to(torch.bfloat16)
+    ref = torch.from_numpy(v @ E2M1[value].T).cuda().float()
+    for t in (3, 17):  # rounded by the kernel, and before it
+        assert torch.equal(lin.quantized(x[:t], dtype=torch.float32), ref[:t])
+    assert torch.equal(lin.quantized(sffn.Mx4Tokens(x), dtype=torch.float32), ref)
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^31 results, and tokens more than 2^31 elements apart."""
     torch, sffn = need_gpu()
